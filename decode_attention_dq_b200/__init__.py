@@ -13,7 +13,9 @@ from ._native import (DQ_BF16, DQ_F32, DQ_STREAM_K, DQ_STREAM_V, DqConfig, DqErr
                       Tables, containers_of, dq_append_kv, dq_append_workspace_bytes, dq_build_tables, dq_config_default,
                       dq_append_kv_paged, dq_decode_attention, dq_decode_attention_noalloc,
                       dq_decode_attention_paged, dq_prefill_attention, dq_prefill_attention_paged,
-                      dq_prefill_workspace_bytes,
+                      dq_prefill_workspace_bytes, dq_decode_attention_window, dq_decode_attention_window_paged,
+                      dq_prefill_attention_window, dq_prefill_attention_window_paged,
+                      dq_prefill_window_workspace_bytes,
                       new_pool,
                       dq_decode_symbols, dq_decode_workspace_bytes,
                       dq_design_stream, dq_error_string, load, new_cache, new_stats,

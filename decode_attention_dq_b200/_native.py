@@ -28,7 +28,9 @@ EXPORTED = ("dq_config_default", "dq_build_tables", "dq_free_tables", "dq_get_st
             "dq_decode_attention", "dq_decode_symbols", "dq_error_string", "dq_last_cuda_error",
             "dq_design_stream", "dq_decode_attention_noalloc", "dq_append_workspace_bytes",
             "dq_append_kv_ws", "dq_append_kv_paged", "dq_decode_attention_paged",
-            "dq_prefill_attention", "dq_prefill_attention_paged", "dq_prefill_workspace_bytes")
+            "dq_prefill_attention", "dq_prefill_attention_paged", "dq_prefill_workspace_bytes",
+            "dq_decode_attention_window", "dq_decode_attention_window_paged", "dq_prefill_attention_window",
+            "dq_prefill_attention_window_paged", "dq_prefill_window_workspace_bytes")
 
 
 class DqConfig(C.Structure):
@@ -97,6 +99,18 @@ def load():
     lib.dq_prefill_attention_paged.argtypes = [vp, vp, C.c_int, vp, vp, i64, vp, i64, vp, C.c_int,
                                                C.c_int, C.c_int, C.c_int, C.c_float, vp, C.c_int, vp,
                                                C.c_size_t, vp, vp]
+    lib.dq_decode_attention_window.argtypes = [vp, vp, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int, i64, i64,
+                                               i64, i64, C.c_float, vp, C.c_int, vp, C.c_size_t, vp, vp]
+    lib.dq_decode_attention_window_paged.argtypes = [vp, vp, C.c_int, vp, vp, i64, vp, i64, vp, C.c_int, C.c_int,
+                                                     C.c_int, i64, i64, i64, C.c_float, vp, C.c_int, vp, C.c_size_t,
+                                                     vp, vp]
+    lib.dq_prefill_window_workspace_bytes.argtypes = [vp, C.c_int, C.c_int, i64, C.c_int, i64, i64]
+    lib.dq_prefill_window_workspace_bytes.restype = C.c_size_t
+    lib.dq_prefill_attention_window.argtypes = [vp, vp, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, i64,
+                                                i64, i64, C.c_float, vp, C.c_int, vp, C.c_size_t, vp, vp]
+    lib.dq_prefill_attention_window_paged.argtypes = [vp, vp, C.c_int, vp, vp, i64, vp, i64, vp, C.c_int, C.c_int,
+                                                      C.c_int, C.c_int, i64, i64, C.c_float, vp, C.c_int, vp,
+                                                      C.c_size_t, vp, vp]
     lib.dq_error_string.argtypes = [C.c_int]
     lib.dq_error_string.restype = C.c_char_p
     lib.dq_last_cuda_error.argtypes = []
@@ -348,6 +362,138 @@ def dq_prefill_attention_paged(tab: Tables, q: torch.Tensor, kpool: torch.Tensor
         _ptr(page_table), page_table.shape[1], _ptr(q_start), B, n_q, Hq, Hkv, float(sm_scale),
         _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _ptr(stats), _stream(stream)))
+
+
+def _check_cuda(**tensors) -> None:
+    """Each tensor on one CUDA device and contiguous (the calls take plain pointers)."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous CUDA tensor" % name)
+        if device is not None and t.device != device:
+            raise ValueError("%s is on %s, the others on %s" % (name, t.device, device))
+        device = t.device
+
+
+def _check_heads(tab, q, out, kcache, vcache):
+    if q.shape[-1] != 128 or out.shape != q.shape:
+        raise ValueError("q and out must have one shape with 128 coordinates, got %s and %s" % (q.shape, out.shape))
+    if kcache.dtype != torch.uint8 or vcache.dtype != torch.uint8 or kcache.dim() != 4 or vcache.dim() != 4:
+        raise ValueError("caches must be 4-dimensional uint8 tensors")
+    if kcache.shape[:2] != vcache.shape[:2]:
+        raise ValueError("K and V caches differ in shape: %s and %s" % (kcache.shape, vcache.shape))
+
+
+def _check_contiguous_cache(tab, B, kcache, vcache):
+    T_cap = kcache.shape[2]
+    want = tuple((B, tab.n_kv_heads, T_cap, s.container_bytes) for s in (tab.k, tab.v))
+    if (tuple(kcache.shape), tuple(vcache.shape)) != want:
+        raise ValueError("caches must be %s and %s, got %s and %s" % (*want, tuple(kcache.shape), tuple(vcache.shape)))
+
+
+def _check_pools(tab, B, kpool, vpool, page_table):
+    want = tuple((kpool.shape[0], tab.n_kv_heads, s.container_bytes, 32) for s in (tab.k, tab.v))
+    if (tuple(kpool.shape), tuple(vpool.shape)) != want:
+        raise ValueError("pools must be %s and %s, got %s and %s" % (*want, tuple(kpool.shape), tuple(vpool.shape)))
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be int32 [%d, max_pages]" % B)
+
+
+def _check_lens(name, t, B):
+    if t.dtype != torch.int32 or tuple(t.shape) != (B,):
+        raise ValueError("%s must be int32 [%d], got %s %s" % (name, B, t.dtype, tuple(t.shape)))
+
+
+def dq_decode_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
+                               seq_lens: torch.Tensor, T_max: int, window: int, sinks: int, out: torch.Tensor,
+                               workspace: torch.Tensor, sm_scale: float | None = None,
+                               stats: torch.Tensor | None = None, stream=None) -> None:
+    """dq_decode_attention over the last `window` tokens and the first `sinks`
+    ones of each sequence; what lies between is never read."""
+    _check_cuda(q=q, kcache=kcache, vcache=vcache, seq_lens=seq_lens, out=out, workspace=workspace, stats=stats)
+    _check_heads(tab, q, out, kcache, vcache)
+    B, Hq, _ = q.shape
+    _check_contiguous_cache(tab, B, kcache, vcache)
+    _check_lens("seq_lens", seq_lens, B)
+    _check("dq_decode_attention_window", load().dq_decode_attention_window(
+        tab.handle, _ptr(q), _dtype_code(q), _ptr(kcache), _ptr(vcache), _ptr(seq_lens), B, Hq, kcache.shape[1],
+        kcache.shape[2], T_max, window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out),
+        _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(stats),
+        _stream(stream)))
+
+
+def dq_decode_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor,
+                                     page_table: torch.Tensor, seq_lens: torch.Tensor, T_max: int, window: int,
+                                     sinks: int, out: torch.Tensor, workspace: torch.Tensor,
+                                     sm_scale: float | None = None, stats: torch.Tensor | None = None,
+                                     stream=None) -> None:
+    """dq_decode_attention_window over page pools; page-table entries between
+    the first tokens and the window may be -1."""
+    _check_cuda(q=q, kpool=kpool, vpool=vpool, page_table=page_table, seq_lens=seq_lens, out=out,
+                workspace=workspace, stats=stats)
+    _check_heads(tab, q, out, kpool, vpool)
+    B, Hq, _ = q.shape
+    _check_pools(tab, B, kpool, vpool, page_table)
+    _check_lens("seq_lens", seq_lens, B)
+    _check("dq_decode_attention_window_paged", load().dq_decode_attention_window_paged(
+        tab.handle, _ptr(q), _dtype_code(q), _ptr(kpool), _ptr(vpool), kpool.shape[0], _ptr(page_table),
+        page_table.shape[1], _ptr(seq_lens), B, Hq, kpool.shape[1], T_max, window, sinks,
+        float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(stats), _stream(stream)))
+
+
+def dq_prefill_window_workspace_bytes(tab: Tables, B: int, Hkv: int, T_cap: int, n_q: int, window: int,
+                                      sinks: int) -> int:
+    """Bytes of the dq_prefill_attention_window workspace (decoded tiles of what a chunk of n_q tokens sees)."""
+    return int(load().dq_prefill_window_workspace_bytes(tab.handle, B, Hkv, T_cap, n_q, window, sinks))
+
+
+def dq_prefill_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
+                                q_start: torch.Tensor, window: int, sinks: int, out: torch.Tensor,
+                                workspace: torch.Tensor | None = None, sm_scale: float | None = None,
+                                stats: torch.Tensor | None = None, stream=None) -> None:
+    """dq_prefill_attention whose query at position p sees the tokens p -
+    window + 1 .. p and the first `sinks` ones; workspace uint8 of
+    dq_prefill_window_workspace_bytes (allocated if None)."""
+    _check_cuda(q=q, kcache=kcache, vcache=vcache, q_start=q_start, out=out, workspace=workspace, stats=stats)
+    _check_heads(tab, q, out, kcache, vcache)
+    B, n_q, Hq, _ = q.shape
+    _check_contiguous_cache(tab, B, kcache, vcache)
+    _check_lens("q_start", q_start, B)
+    if workspace is None:
+        workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kcache.shape[1], kcache.shape[2], n_q,
+                                                                  window, sinks), dtype=torch.uint8, device=q.device)
+    _check("dq_prefill_attention_window", load().dq_prefill_attention_window(
+        tab.handle, _ptr(q), _dtype_code(q), _ptr(kcache), _ptr(vcache), _ptr(q_start), B, n_q, Hq, kcache.shape[1],
+        kcache.shape[2], window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out),
+        _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(stats),
+        _stream(stream)))
+
+
+def dq_prefill_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch.Tensor, vpool: torch.Tensor,
+                                      page_table: torch.Tensor, q_start: torch.Tensor, window: int, sinks: int,
+                                      out: torch.Tensor, workspace: torch.Tensor | None = None,
+                                      sm_scale: float | None = None, stats: torch.Tensor | None = None,
+                                      stream=None) -> None:
+    """dq_prefill_attention_window over page pools; page-table entries that no
+    query of the chunk sees may be -1."""
+    _check_cuda(q=q, kpool=kpool, vpool=vpool, page_table=page_table, q_start=q_start, out=out,
+                workspace=workspace, stats=stats)
+    _check_heads(tab, q, out, kpool, vpool)
+    B, n_q, Hq, _ = q.shape
+    _check_pools(tab, B, kpool, vpool, page_table)
+    _check_lens("q_start", q_start, B)
+    if workspace is None:
+        workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kpool.shape[1], 32 * page_table.shape[1],
+                                                                  n_q, window, sinks),
+                                dtype=torch.uint8, device=q.device)
+    _check("dq_prefill_attention_window_paged", load().dq_prefill_attention_window_paged(
+        tab.handle, _ptr(q), _dtype_code(q), _ptr(kpool), _ptr(vpool), kpool.shape[0], _ptr(page_table),
+        page_table.shape[1], _ptr(q_start), B, n_q, Hq, kpool.shape[1], window, sinks,
+        float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(stats), _stream(stream)))
 
 
 def dq_decode_symbols(tab: Tables, cache: torch.Tensor, kind: int, syms: torch.Tensor,

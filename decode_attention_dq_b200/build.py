@@ -25,6 +25,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
     "--expt-relaxed-constexpr",
     "-cudart", "static",
+    "--threads", "0",  # one compilation per core
 ]
 
 

@@ -360,6 +360,13 @@ int dq_append_kv(const dq_tables *t, const void *k, const void *v, int dtype, in
                          d_stats, stream);
 }
 
+static int check_page_table(const int32_t *d_page_table, int64_t num_pages, int64_t max_pages) {
+  if (!d_page_table) return DQ_ERR_NULL;
+  if (num_pages < 1 || max_pages < 1 || max_pages > (int64_t(1) << 40) || num_pages > (int64_t(1) << 31))
+    return DQ_ERR_SHAPE;
+  return aligned(d_page_table, 4) ? DQ_OK : DQ_ERR_ALIGN;
+}
+
 // Shared by dq_append_kv_ws (page_table NULL) and dq_append_kv_paged.
 static int append_core(const dq_tables *t, const void *k, const void *v, int dtype, int B, int Hkv, int n_new,
                        const int32_t *d_start_pos, uint8_t *d_kcache, uint8_t *d_vcache, int64_t T_cap,
@@ -423,10 +430,8 @@ int dq_append_kv_paged(const dq_tables *t, const void *k, const void *v, int dty
                        const int32_t *d_start_pos, uint8_t *d_kpool, uint8_t *d_vpool, int64_t num_pages,
                        const int32_t *d_page_table, int64_t max_pages, void *d_workspace, size_t ws_bytes,
                        dq_stats *d_stats, void *stream) {
-  if (!d_page_table) return DQ_ERR_NULL;
-  if (num_pages < 1 || max_pages < 1 || max_pages > (int64_t(1) << 40) || num_pages > (int64_t(1) << 31))
-    return DQ_ERR_SHAPE;
-  if (!aligned(d_page_table, 4)) return DQ_ERR_ALIGN;
+  const int rc = check_page_table(d_page_table, num_pages, max_pages);
+  if (rc != DQ_OK) return rc;
   return append_core(t, k, v, dtype, B, Hkv, n_new, d_start_pos, d_kpool, d_vpool, 32 * max_pages, d_workspace,
                      ws_bytes, d_stats, stream, d_page_table, max_pages, num_pages);
 }
@@ -436,12 +441,20 @@ size_t dq_decode_workspace_bytes(const dq_tables *t, int B, int Hq, int Hkv, int
   return ws_layout(t, B, Hkv, Hq / Hkv).total;
 }
 
-// Shared by dq_decode_attention (page_table NULL) and dq_decode_attention_paged.
+// Window arguments: at least the query's own token is visible, and scores are
+// masked before they are scaled.
+static int check_window(int64_t window, int64_t sinks, float sm_scale) {
+  return window < 1 || sinks < 0 || !(sm_scale > 0.0f) ? DQ_ERR_SHAPE : DQ_OK;
+}
+
+// Shared by the dq_decode_attention calls (page_table NULL: contiguous cache;
+// window 0: none).
 static int decode_core(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kcache,
                        const uint8_t *d_vcache, const int32_t *d_seq_lens, int B, int Hq, int Hkv,
                        int64_t T_cap, int64_t T_max, float sm_scale, void *out, int out_dtype,
                        void *d_workspace, size_t ws_bytes, dq_stats *d_stats, void *stream,
-                       const int32_t *page_table, int64_t max_pages, int64_t num_pages) {
+                       const int32_t *page_table, int64_t max_pages, int64_t num_pages, int64_t window = 0,
+                       int64_t sinks = 0) {
   try {
     if (!t || !q || !d_kcache || !d_vcache || !d_seq_lens || !out || !d_workspace) return DQ_ERR_NULL;
     if ((q_dtype != DQ_F32 && q_dtype != DQ_BF16) || (out_dtype != DQ_F32 && out_dtype != DQ_BF16))
@@ -491,6 +504,9 @@ static int decode_core(const dq_tables *t, const void *q, int q_dtype, const uin
     a.page_table = page_table;
     a.max_pages = max_pages;
     a.num_pages = num_pages;
+    // (A window of T_cap tokens or more hides nothing; at least 1 keeps the windowed kernel.)
+    a.window = window > 0 ? std::max<int64_t>(1, std::min(window, T_cap)) : 0;
+    a.sinks = std::min(sinks, T_cap);
     int e = dqi::launch_decode_attention(a, stream);
     return e == 0 ? DQ_OK : cuda_fail(static_cast<cudaError_t>(e));
   } catch (...) {
@@ -511,19 +527,47 @@ int dq_decode_attention_paged(const dq_tables *t, const void *q, int q_dtype, co
                               int64_t max_pages, const int32_t *d_seq_lens, int B, int Hq, int Hkv,
                               int64_t T_max, float sm_scale, void *out, int out_dtype, void *d_workspace,
                               size_t ws_bytes, dq_stats *d_stats, void *stream) {
-  if (!d_page_table) return DQ_ERR_NULL;
-  if (num_pages < 1 || max_pages < 1 || max_pages > (int64_t(1) << 40) || num_pages > (int64_t(1) << 31))
-    return DQ_ERR_SHAPE;
-  if (!aligned(d_page_table, 4)) return DQ_ERR_ALIGN;
+  const int rc = check_page_table(d_page_table, num_pages, max_pages);
+  if (rc != DQ_OK) return rc;
   return decode_core(t, q, q_dtype, d_kpool, d_vpool, d_seq_lens, B, Hq, Hkv, 32 * max_pages, T_max, sm_scale,
                      out, out_dtype, d_workspace, ws_bytes, d_stats, stream, d_page_table, max_pages, num_pages);
+}
+
+int dq_decode_attention_window(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kcache,
+                               const uint8_t *d_vcache, const int32_t *d_seq_lens, int B, int Hq, int Hkv,
+                               int64_t T_cap, int64_t T_max, int64_t window, int64_t sinks, float sm_scale,
+                               void *out, int out_dtype, void *d_workspace, size_t ws_bytes, dq_stats *d_stats,
+                               void *stream) {
+  const int rc = check_window(window, sinks, sm_scale);
+  if (rc != DQ_OK) return rc;
+  return decode_core(t, q, q_dtype, d_kcache, d_vcache, d_seq_lens, B, Hq, Hkv, T_cap, T_max, sm_scale, out,
+                     out_dtype, d_workspace, ws_bytes, d_stats, stream, nullptr, 0, 0, window, sinks);
+}
+
+int dq_decode_attention_window_paged(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kpool,
+                                     const uint8_t *d_vpool, int64_t num_pages, const int32_t *d_page_table,
+                                     int64_t max_pages, const int32_t *d_seq_lens, int B, int Hq, int Hkv,
+                                     int64_t T_max, int64_t window, int64_t sinks, float sm_scale, void *out,
+                                     int out_dtype, void *d_workspace, size_t ws_bytes, dq_stats *d_stats,
+                                     void *stream) {
+  int rc = check_page_table(d_page_table, num_pages, max_pages);
+  if (rc == DQ_OK) rc = check_window(window, sinks, sm_scale);
+  if (rc != DQ_OK) return rc;
+  return decode_core(t, q, q_dtype, d_kpool, d_vpool, d_seq_lens, B, Hq, Hkv, 32 * max_pages, T_max, sm_scale, out,
+                     out_dtype, d_workspace, ws_bytes, d_stats, stream, d_page_table, max_pages, num_pages, window,
+                     sinks);
+}
+
+// Bytes of one (b, KV head) row of the prefill workspace.
+static size_t prefill_row_bytes(int64_t T_cap, int n_q, int64_t window, int64_t sinks) {
+  return static_cast<size_t>(dqi::prefill_row_slots(T_cap, n_q, window, sinks)) * dqi::prefill_slot_bytes();
 }
 
 static int prefill_core(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kcache,
                         const uint8_t *d_vcache, const int32_t *d_q_start, int B, int n_q, int Hq, int Hkv,
                         int64_t T_cap, float sm_scale, void *out, int out_dtype, void *d_workspace,
                         size_t ws_bytes, dq_stats *d_stats, void *stream, const int32_t *page_table,
-                        int64_t max_pages, int64_t num_pages) {
+                        int64_t max_pages, int64_t num_pages, int64_t window = 0, int64_t sinks = 0) {
   try {
     if (!t || !q || !d_kcache || !d_vcache || !d_q_start || !out || !d_workspace) return DQ_ERR_NULL;
     if ((q_dtype != DQ_F32 && q_dtype != DQ_BF16) || (out_dtype != DQ_F32 && out_dtype != DQ_BF16))
@@ -541,7 +585,10 @@ static int prefill_core(const dq_tables *t, const void *q, int q_dtype, const ui
     // at least one row; a smaller workspace than the whole batch's runs the
     // call in several waves.
     const int64_t rows = static_cast<int64_t>(B) * Hkv;
-    const size_t row_bytes = dqi::prefill_workspace_bytes(1, 1, T_cap);
+    // (A window of T_cap tokens or more hides nothing; at least 1 keeps the windowed kernels.)
+    window = window > 0 ? std::max<int64_t>(1, std::min(window, T_cap)) : 0;
+    sinks = std::min(sinks, T_cap);
+    const size_t row_bytes = prefill_row_bytes(T_cap, n_q, window, sinks);
     if (T_cap > 0 && ws_bytes < row_bytes) return DQ_ERR_WORKSPACE;
     const int64_t per_wave = row_bytes ? std::min<int64_t>(rows, static_cast<int64_t>(ws_bytes / row_bytes)) : rows;
     if (per_wave > 0 && dqi::prefill_grid(per_wave, G, n_q) > 0x7FFFFFFF) return DQ_ERR_SHAPE;
@@ -578,6 +625,9 @@ static int prefill_core(const dq_tables *t, const void *q, int q_dtype, const ui
     a.two_v = has_small_freq(t->v);
     a.tiles = static_cast<uint8_t *>(d_workspace);
     a.nslots = dqi::prefill_ring_slots();
+    a.window = window;
+    a.sinks = sinks;
+    a.row_slots = dqi::prefill_row_slots(T_cap, n_q, window, sinks);
     a.stats = d_stats;
     a.page_table = page_table;
     a.max_pages = max_pages;
@@ -585,7 +635,7 @@ static int prefill_core(const dq_tables *t, const void *q, int q_dtype, const ui
     for (int64_t bh0 = 0; bh0 < rows; bh0 += per_wave) {
       a.bh0 = bh0;
       a.nbh = std::min<int64_t>(per_wave, rows - bh0);
-      const int64_t groups = a.nbh * (T_cap / 32);
+      const int64_t groups = a.nbh * std::min<int64_t>(T_cap / 32, a.row_slots * 4);
       a.tile_grid = static_cast<int>(std::min<int64_t>(t->sm_count, (groups + 19) / 20));
       int e = dqi::launch_prefill_attention(a, stream);
       if (e != 0) return cuda_fail(static_cast<cudaError_t>(e));
@@ -598,7 +648,14 @@ static int prefill_core(const dq_tables *t, const void *q, int q_dtype, const ui
 
 size_t dq_prefill_workspace_bytes(const dq_tables *t, int B, int Hkv, int64_t T_cap) {
   if (!t || B < 0 || Hkv < 1 || T_cap < 0 || T_cap % 32) return 0;
-  return std::max<size_t>(16, dqi::prefill_workspace_bytes(B, Hkv, T_cap));
+  return std::max<size_t>(16, static_cast<size_t>(B) * Hkv * prefill_row_bytes(T_cap, 0, 0, 0));
+}
+
+size_t dq_prefill_window_workspace_bytes(const dq_tables *t, int B, int Hkv, int64_t T_cap, int n_q, int64_t window,
+                                         int64_t sinks) {
+  if (!t || B < 0 || Hkv < 1 || T_cap < 0 || T_cap % 32 || n_q < 0 || window < 1 || sinks < 0) return 0;
+  window = std::max<int64_t>(1, std::min(window, T_cap));
+  return std::max<size_t>(16, static_cast<size_t>(B) * Hkv * prefill_row_bytes(T_cap, n_q, window, std::min(sinks, T_cap)));
 }
 
 int dq_prefill_attention(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kcache,
@@ -614,12 +671,33 @@ int dq_prefill_attention_paged(const dq_tables *t, const void *q, int q_dtype, c
                                int64_t max_pages, const int32_t *d_q_start, int B, int n_q, int Hq, int Hkv,
                                float sm_scale, void *out, int out_dtype, void *d_workspace, size_t ws_bytes,
                                dq_stats *d_stats, void *stream) {
-  if (!d_page_table) return DQ_ERR_NULL;
-  if (num_pages < 1 || max_pages < 1 || max_pages > (int64_t(1) << 40) || num_pages > (int64_t(1) << 31))
-    return DQ_ERR_SHAPE;
-  if (!aligned(d_page_table, 4)) return DQ_ERR_ALIGN;
+  const int rc = check_page_table(d_page_table, num_pages, max_pages);
+  if (rc != DQ_OK) return rc;
   return prefill_core(t, q, q_dtype, d_kpool, d_vpool, d_q_start, B, n_q, Hq, Hkv, 32 * max_pages, sm_scale, out,
                       out_dtype, d_workspace, ws_bytes, d_stats, stream, d_page_table, max_pages, num_pages);
+}
+
+int dq_prefill_attention_window(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kcache,
+                                const uint8_t *d_vcache, const int32_t *d_q_start, int B, int n_q, int Hq, int Hkv,
+                                int64_t T_cap, int64_t window, int64_t sinks, float sm_scale, void *out,
+                                int out_dtype, void *d_workspace, size_t ws_bytes, dq_stats *d_stats, void *stream) {
+  const int rc = check_window(window, sinks, sm_scale);
+  if (rc != DQ_OK) return rc;
+  return prefill_core(t, q, q_dtype, d_kcache, d_vcache, d_q_start, B, n_q, Hq, Hkv, T_cap, sm_scale, out, out_dtype,
+                      d_workspace, ws_bytes, d_stats, stream, nullptr, 0, 0, window, sinks);
+}
+
+int dq_prefill_attention_window_paged(const dq_tables *t, const void *q, int q_dtype, const uint8_t *d_kpool,
+                                      const uint8_t *d_vpool, int64_t num_pages, const int32_t *d_page_table,
+                                      int64_t max_pages, const int32_t *d_q_start, int B, int n_q, int Hq, int Hkv,
+                                      int64_t window, int64_t sinks, float sm_scale, void *out, int out_dtype,
+                                      void *d_workspace, size_t ws_bytes, dq_stats *d_stats, void *stream) {
+  int rc = check_page_table(d_page_table, num_pages, max_pages);
+  if (rc == DQ_OK) rc = check_window(window, sinks, sm_scale);
+  if (rc != DQ_OK) return rc;
+  return prefill_core(t, q, q_dtype, d_kpool, d_vpool, d_q_start, B, n_q, Hq, Hkv, 32 * max_pages, sm_scale, out,
+                      out_dtype, d_workspace, ws_bytes, d_stats, stream, d_page_table, max_pages, num_pages, window,
+                      sinks);
 }
 
 int dq_decode_symbols(const dq_tables *t, const uint8_t *d_cache, int stream_kind,

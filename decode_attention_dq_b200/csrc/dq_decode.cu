@@ -40,6 +40,11 @@
 // Combine kernel, one CTA per (b, query head), of 16 warps for small batches
 // (hundreds of slots per row) and 4 otherwise:
 //   D7  log-sum-exp merge of the slots of (b, h), o = D H o_rot / (128 l)
+//
+// With a sliding window (kWin) the flat order holds the visible groups only:
+// of each sequence the groups of the first tokens, then those from the
+// window's first token on. Nothing else changes: the hidden groups take no
+// place in the order, their bytes and page-table entries are never read.
 #include <type_traits>
 
 #include "dq_device.cuh"
@@ -270,11 +275,28 @@ __device__ __forceinline__ void softmax_update(WarpAcc<G> &acc, const float (&sc
   }
 }
 
+// fp16 norm of a staged container; the encoder stores finite norms only, so
+// any other belongs to a corrupt container and counts as 0.
+__device__ __forceinline__ float finite_norm_of(const uint8_t *cb) {
+  return (cb[kTile] & 0x7C) == 0x7C ? 0.0f : norm_of(cb);
+}
+
 __device__ __forceinline__ int64_t clamp_len(int32_t len, int64_t cap) {
   int64_t v = len;
   if (v < 0) v = 0;
   if (v > cap) v = cap;
   return v;
+}
+
+// Visible token groups of a sequence of len tokens.
+template <bool kWin>
+__device__ __forceinline__ WindowSpan visible_groups(const DecodeArgs &a, int64_t len) {
+  if constexpr (kWin) return window_span(len > a.window ? len - a.window : 0, len, a.sinks, kTile);
+  WindowSpan s;
+  s.head = 0;
+  s.skip = 0;
+  s.n = (len + kTile - 1) / kTile;
+  return s;
 }
 
 // First flat group index of warp w out of W over N groups (warp w owns
@@ -292,6 +314,7 @@ __host__ __device__ __forceinline__ int64_t active_warps(int64_t total, int64_t 
 // also counts the sequence lengths that had to be clamped.
 constexpr int kPrefixThreads = 1024;
 
+template <bool kWin>
 __global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const DecodeArgs a) {
   __shared__ int64_t warp_tot[kPrefixThreads / 32];
   __shared__ int64_t carry_s;
@@ -309,7 +332,7 @@ __global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const DecodeArgs
     if (i < a.B) {
       const int32_t len = a.seq_lens[i];
       if (len < 0 || len > cap) ++clamped;
-      v = (clamp_len(len, cap) + kTile - 1) / kTile;
+      v = visible_groups<kWin>(a, clamp_len(len, cap)).n;
     }
     int64_t inc = v;
 #pragma unroll
@@ -336,7 +359,7 @@ __global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const DecodeArgs
 // enough registers for its larger accumulators.
 __host__ __device__ constexpr int max_warps_for(int G) { return G >= 8 ? 12 : kMaxWarps; }
 
-template <int G, bool kTwoK, bool kTwoV>
+template <int G, bool kTwoK, bool kTwoV, bool kWin>
 __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int nwarps = blockDim.x >> 5;
@@ -428,13 +451,34 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
     }
 
     const int64_t tseg = j0 * kTile;
-    auto group_t0 = [&](int64_t j) { return tseg + j * kTile; };
+    const WindowSpan span = visible_groups<kWin>(a, len);
+    // First token of group j of the segment.
+    auto group_t0 = [&](int64_t j) {
+      if constexpr (kWin) return span.block(j0 + j) * kTile;
+      return tseg + j * kTile;
+    };
+    // Whether this lane's token of the group at t0 is visible.
+    auto visible = [&](int64_t t0) {
+      const int64_t t = t0 + lane;
+      if constexpr (kWin) return t < len && (t < a.sinks || t >= len - a.window);
+      return t < len;
+    };
+    auto norm_at = [&](const uint8_t *cb) {
+      if constexpr (kWin) return finite_norm_of(cb);
+      return norm_of(cb);
+    };
+    // Containers of one stream that did not decode to the initial state.
+    auto count_bad = [&](bool seen, const RansLane &r, const uint8_t *cb) {
+      bool bad = r.x != kL;
+      if constexpr (kWin) bad = bad || (cb[kTile] & 0x7C) == 0x7C;
+      bad_count += __popc(__ballot_sync(kFull, seen && bad));
+    };
     // Cache block (32 tokens of one KV head) holding group j of the segment:
     // block b of a cache sits at byte 32 C b. Contiguous caches: row bh,
     // token block t / 32. Paged caches: page_table[b][t / 32] * Hkv + h; an
     // entry out of range is counted and read as page 0 (garbage, no fault).
     auto block_of = [&](int64_t j) -> int64_t {
-      const int64_t tb = (tseg >> 5) + j;
+      const int64_t tb = kWin ? span.block(j0 + j) : (tseg >> 5) + j;
       if (a.page_table) {
         int64_t pg = a.page_table[static_cast<int64_t>(b) * a.max_pages + tb];
         if (pg < 0 || pg >= a.num_pages) {
@@ -491,12 +535,12 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
         const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + ek);
         score_fma<G>(sc, qt + i * G, yk);
       }
-      const bool valid = group_t0(0) + lane < len;
-      bad_count += __popc(__ballot_sync(kFull, valid && rk.x != kL));
+      const bool valid = visible(group_t0(0));
+      count_bad(valid, rk, kb);
 #ifdef DQ_CHECKED
       over_count += __popc(__ballot_sync(kFull, valid && overread(rk, kb, smem, ck)));
 #endif
-      softmax_update(acc, sc, norm_of(kb), valid, p, lane);
+      softmax_update(acc, sc, norm_at(kb), valid, p, lane);
     }
     for (int64_t j = 0; j < n; ++j) {
       const int cur = static_cast<int>(j & 1), nxt = cur ^ 1;
@@ -508,8 +552,8 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
       uint32_t fb_hi[2][2], fb_lo[2][2];
       {
         const uint8_t *vb = vst + cur * kTile * cv + lane;
-        const bool valid = group_t0(j) + lane < len;
-        const float nv = norm_of(vb);
+        const bool valid = visible(group_t0(j));
+        const float nv = norm_at(vb);
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const float w = valid ? p[gg] * nv : 0.0f;
@@ -578,19 +622,19 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
       run_half(std::integral_constant<int, 0>{});
       run_half(std::integral_constant<int, 1>{});
       {
-        const bool vvalid = group_t0(j) + lane < len;
-        bad_count += __popc(__ballot_sync(kFull, vvalid && rv.x != kL));
+        const bool vvalid = visible(group_t0(j));
+        count_bad(vvalid, rv, vb);
 #ifdef DQ_CHECKED
         over_count += __popc(__ballot_sync(kFull, vvalid && overread(rv, vb, smem, cv)));
 #endif
       }
       if (has_next) {
-        const bool valid = group_t0(j + 1) + lane < len;
-        bad_count += __popc(__ballot_sync(kFull, valid && rk.x != kL));
+        const bool valid = visible(group_t0(j + 1));
+        count_bad(valid, rk, kb);
 #ifdef DQ_CHECKED
         over_count += __popc(__ballot_sync(kFull, valid && overread(rk, kb, smem, ck)));
 #endif
-        softmax_update(acc, sc, norm_of(kb), valid, p, lane);
+        softmax_update(acc, sc, norm_at(kb), valid, p, lane);
         // The next iteration needs V(j+1) (slot nxt) and K(j+2) (slot cur).
         cp_async_wait_0();
         __syncwarp();
@@ -735,24 +779,39 @@ int warps_for(int G, int ck, int cv) {
   return nw;
 }
 
-template <int G, bool kTwoK, bool kTwoV>
+template <int G, bool kTwoK, bool kTwoV, bool kWin>
 int launch_split(const DecodeArgs &a, cudaStream_t st) {
   const int nw = warps_for(G, a.ck, a.cv);
   if (static_cast<int64_t>(a.grid) * nw != a.total_warps) return static_cast<int>(cudaErrorInvalidValue);
   const SplitSmem L = split_smem_layout(G, a.ck, a.cv, nw);
-  constexpr auto kern = decode_split_kernel<G, kTwoK, kTwoV>;
+  constexpr auto kern = decode_split_kernel<G, kTwoK, kTwoV, kWin>;
   const cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
   if (e != cudaSuccess) return static_cast<int>(e);
   kern<<<a.grid, nw * 32, L.total, st>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
-template <int G>
+template <int G, bool kWin>
 int launch_split_g(const DecodeArgs &a, cudaStream_t st) {
-  if (a.two_k && a.two_v) return launch_split<G, true, true>(a, st);
-  if (a.two_k) return launch_split<G, true, false>(a, st);
-  if (a.two_v) return launch_split<G, false, true>(a, st);
-  return launch_split<G, false, false>(a, st);
+  if (a.two_k && a.two_v) return launch_split<G, true, true, kWin>(a, st);
+  if (a.two_k) return launch_split<G, true, false, kWin>(a, st);
+  if (a.two_v) return launch_split<G, false, true, kWin>(a, st);
+  return launch_split<G, false, false, kWin>(a, st);
+}
+
+// Prefix and split kernels.
+template <bool kWin>
+int launch_groups(const DecodeArgs &a, cudaStream_t st) {
+  prefix_kernel<kWin><<<1, kPrefixThreads, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  switch (a.G) {
+    case 1: return launch_split_g<1, kWin>(a, st);
+    case 2: return launch_split_g<2, kWin>(a, st);
+    case 4: return launch_split_g<4, kWin>(a, st);
+    case 8: return launch_split_g<8, kWin>(a, st);
+    default: return static_cast<int>(cudaErrorInvalidValue);
+  }
 }
 
 }  // namespace
@@ -766,17 +825,7 @@ int decode_warps_per_cta(int G, int ck, int cv) {
 int launch_decode_attention(const DecodeArgs &a, void *stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.ck > kMaxContainer || a.cv > kMaxContainer || a.grid < 1) return static_cast<int>(cudaErrorInvalidValue);
-  prefix_kernel<<<1, kPrefixThreads, 0, st>>>(a);
-  const cudaError_t ce = cudaGetLastError();
-  if (ce != cudaSuccess) return static_cast<int>(ce);
-  int e = 0;
-  switch (a.G) {
-    case 1: e = launch_split_g<1>(a, st); break;
-    case 2: e = launch_split_g<2>(a, st); break;
-    case 4: e = launch_split_g<4>(a, st); break;
-    case 8: e = launch_split_g<8>(a, st); break;
-    default: return static_cast<int>(cudaErrorInvalidValue);
-  }
+  const int e = a.window > 0 ? launch_groups<true>(a, st) : launch_groups<false>(a, st);
   if (e) return e;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
   if (rows > 0x7FFFFFFF) return static_cast<int>(cudaErrorInvalidValue);

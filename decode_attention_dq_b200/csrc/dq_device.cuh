@@ -92,6 +92,26 @@ cudaError_t ensure_max_dynamic_smem(int bytes) {
   return e;
 }
 
+// What a sliding window leaves of a run of blocks: the blocks that hold the
+// first tokens, then, `skip` blocks further, the blocks from the window's
+// first token to the last one. Visible block j is block j (j < head) or
+// j + skip; n of them.
+struct WindowSpan {
+  int64_t head, skip, n;
+  __host__ __device__ __forceinline__ int64_t block(int64_t j) const { return j < head ? j : j + skip; }
+};
+
+// The visible blocks of `blk` tokens for tokens [0, sinks) and [lo, end), with
+// 0 <= lo < end (or end = 0: none). Blocks that hold both are counted once.
+__host__ __device__ __forceinline__ WindowSpan window_span(int64_t lo, int64_t end, int64_t sinks, int blk) {
+  WindowSpan s;
+  const int64_t first = (sinks + blk - 1) / blk, w0 = lo / blk;
+  s.head = first < w0 ? first : w0;
+  s.skip = w0 - s.head;
+  s.n = (end + blk - 1) / blk - s.skip;
+  return s;
+}
+
 // Sign of coordinate lane + 32 k for a KV head: bit `lane` of sign word k.
 __device__ __forceinline__ float apply_sign(float v, uint32_t word, int lane) {
   return ((word >> lane) & 1u) ? -v : v;

@@ -124,6 +124,9 @@ struct DecodeArgs {
   // Paged caches, as in AppendArgs (nullptr: contiguous).
   const int32_t *page_table;
   int64_t max_pages, num_pages;
+  // Sliding window (0: none): token t of len is visible when t >= len -
+  // window or t < sinks. Both at most T_cap.
+  int64_t window, sinks;
 };
 int launch_decode_attention(const DecodeArgs &a, void *stream);
 // Warps per CTA of the split kernel for these shapes (0 if unsupported).
@@ -151,13 +154,20 @@ struct PrefillArgs {
   dq_stats *stats;
   const int32_t *page_table;  // paged caches as in AppendArgs (nullptr: contiguous)
   int64_t max_pages, num_pages;
+  // Sliding window (0: none): token t is visible to a query at position p >= t
+  // when t > p - window or t < sinks. Both at most T_cap.
+  int64_t window, sinks;
+  int64_t row_slots;   // workspace slots per (b, KV head) row (prefill_row_slots)
 };
 int launch_prefill_attention(const PrefillArgs &a, void *stream);
 int prefill_ring_slots();
 // CTAs of the attention kernel for nbh rows: nbh * ceil(n_q / (128 / G)).
 int64_t prefill_grid(int64_t nbh, int G, int n_q);
-// Bytes of decoded slots for B x Hkv rows of T_cap tokens.
-size_t prefill_workspace_bytes(int B, int Hkv, int64_t T_cap);
+// Workspace slots of one (b, KV head) row: every 128-token block of the cache
+// (window 0), or the most that a chunk of n_q tokens can attend to.
+int64_t prefill_row_slots(int64_t T_cap, int n_q, int64_t window, int64_t sinks);
+// Bytes of one such slot.
+size_t prefill_slot_bytes();
 bool prefill_supported(int ck, int cv);
 
 struct SymbolsArgs {

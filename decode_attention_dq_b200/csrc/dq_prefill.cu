@@ -55,6 +55,11 @@
 //        copies counted on mbarriers.
 // The softmax arithmetic runs in packed fp32x2 operations (two tokens per
 // instruction) and three-input maxima.
+// With a sliding window (kWin) a chunk attends to the 128-token blocks of the
+// first tokens and to those from its first query's window on. The workspace
+// holds these slots only, one behind the other, and each CTA walks the part
+// of them that its own 128 / G query tokens see; the rest of a long cache is
+// neither decoded nor read, whatever the page table says there.
 // Every wait is bounded; a CTA that gives up counts it in wait_timeouts,
 // skips the rest of its work and still frees its tensor memory after its MMAs
 // and copies have drained.
@@ -148,6 +153,13 @@ __host__ __device__ inline AttnSmem attn_smem_layout(int nslots) {
 __host__ __device__ __forceinline__ int64_t last_position(int64_t qs, int n_q, int64_t T_cap) {
   if (qs > T_cap - 1 || qs + n_q - 1 < 0) return -1;
   return qs + n_q - 1 < T_cap - 1 ? qs + n_q - 1 : T_cap - 1;
+}
+
+// First position that the window of the chunk's first query inside the cache
+// reaches.
+__host__ __device__ __forceinline__ int64_t window_start(int64_t qs, int64_t window) {
+  const int64_t p = qs > 0 ? qs : 0;
+  return p + 1 > window ? p + 1 - window : 0;
 }
 
 // ---- PTX wrappers -------------------------------------------------------
@@ -426,9 +438,11 @@ __device__ __forceinline__ uint32_t rans_step(RansLane &r, const uint32_t *lut, 
 __device__ __forceinline__ float norm_of(const uint8_t *cb) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(cb[0] | (cb[kGrp] << 8))));
 }
+// Whether a staged container's fp16 norm is infinite or NaN (the encoder
+// stores finite norms only: a corrupt container).
+__device__ __forceinline__ bool norm_not_finite(const uint8_t *cb) { return (cb[kGrp] & 0x7C) == 0x7C; }
 
-
-template <bool kTwoK, bool kTwoV>
+template <bool kTwoK, bool kTwoV, bool kWin>
 __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const PrefillArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const TilesSmem L = tiles_smem_layout(a.ck, a.cv);
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
   __syncthreads();
 
   const int ck = a.ck, cv = a.cv;
-  const int64_t gslots = (a.T_cap + kBlk - 1) / kBlk;  // slots per (b, h)
+  const int64_t gslots = kWin ? a.row_slots : (a.T_cap + kBlk - 1) / kBlk;  // slots per (b, h)
   constexpr int kQuarters = kBlk / kGrp;
   // Work unit u = ((row - bh0) gslots + slot) * 4 + quarter, row = b Hkv + h
   // of this wave: one 32-token group of one slot.
@@ -466,14 +480,16 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
 #ifdef DQ_CHECKED
   unsigned over = 0;  // containers decoded past their C bytes
 #endif
-  auto last_of = [&](int64_t u) -> int64_t {
-    return last_position(a.q_start[(a.bh0 + u / (gslots * kQuarters)) / a.Hkv], a.n_q, a.T_cap);
-  };
+  auto start_of = [&](int64_t u) -> int64_t { return a.q_start[(a.bh0 + u / (gslots * kQuarters)) / a.Hkv]; };
+  auto last_of = [&](int64_t u) -> int64_t { return last_position(start_of(u), a.n_q, a.T_cap); };
+  // The slots of the unit's row that its chunk attends to (kWin).
+  auto span_of = [&](int64_t u, int64_t hi) { return window_span(window_start(start_of(u), a.window), hi + 1, a.sinks, kBlk); };
   // Next unit >= u (in steps of W) inside a slot the chunk attends to.
   auto next_valid = [&](int64_t u) -> int64_t {
     for (; u < total; u += W) {
       const int64_t hi = last_of(u);
-      if (hi >= 0 && (u / kQuarters) % gslots <= hi / kBlk) return u;
+      if (kWin ? hi >= 0 && (u / kQuarters) % gslots < span_of(u, hi).n : hi >= 0 && (u / kQuarters) % gslots <= hi / kBlk)
+        return u;
     }
     return total;
   };
@@ -490,10 +506,23 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
     }
     return bh * (a.T_cap / kGrp) + j;
   };
-  auto group_of = [&](int64_t u) -> int64_t { return ((u / kQuarters) % gslots) * kQuarters + u % kQuarters; };
+  auto group_of = [&](int64_t u) -> int64_t {
+    const int64_t slot = (u / kQuarters) % gslots;
+    return (kWin ? span_of(u, last_of(u)).block(slot) : slot) * kQuarters + u % kQuarters;
+  };
   // Units whose group holds an attended token are decoded; the others (past
   // the last attended position, possibly past the cache) are zero-filled.
-  auto decoded = [&](int64_t u) { return group_of(u) * kGrp <= last_of(u); };
+  // With a window, neither are those between the first tokens and the window.
+  auto attended = [&](int64_t u, int64_t tok) {
+    if constexpr (kWin) return tok <= last_of(u) && (tok < a.sinks || tok >= window_start(start_of(u), a.window));
+    return tok <= last_of(u);
+  };
+  auto decoded = [&](int64_t u) {
+    const int64_t t0 = group_of(u) * kGrp;
+    if constexpr (kWin)
+      return t0 <= last_of(u) && (t0 < a.sinks || t0 + kGrp > window_start(start_of(u), a.window));
+    return t0 <= last_of(u);
+  };
   auto stage = [&](int sl, int64_t u) {
     const int64_t blk = block_of(u, group_of(u));
     const uint8_t *ks = a.kcache + blk * kGrp * ck;
@@ -540,20 +569,22 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
             make_uint4(__byte_perm(hv[0], hv[1], 0x5410), __byte_perm(hv[2], hv[3], 0x5410),
                        __byte_perm(hv[4], hv[5], 0x5410), __byte_perm(hv[6], hv[7], 0x5410));
       }
-      const int64_t hi = last_of(u);
-      const int64_t tok = group_of(u) * kGrp + lane;
-      // Tokens past the last attended position keep zero norms: their bytes
-      // may be anything, and the softmax multiplies the weights by them.
-      nrm[tl] = tok <= hi ? norm_of(kb) : 0.0f;
-      const float nvt = tok <= hi ? norm_of(vb) : 0.0f;
+      // Tokens that no row attends to keep zero norms: their bytes may be
+      // anything, and the softmax multiplies the weights by them. (kWin: nor
+      // does a corrupt container's infinite or NaN norm reach the rows that
+      // do not see its token.)
+      const bool att = attended(u, group_of(u) * kGrp + lane);
+      const bool bad_k = kWin && norm_not_finite(kb), bad_v = kWin && norm_not_finite(vb);
+      nrm[tl] = att && !bad_k ? norm_of(kb) : 0.0f;
+      const float nvt = att && !bad_v ? norm_of(vb) : 0.0f;
       nrm[kBlk + tl] = nvt;
       // The quarter's largest V norm (bounds the softmax weights of a block).
       const float qm = warp_max(nvt);
       if (lane == 0) reinterpret_cast<float *>(dst + kQmaxOff)[q4] = qm;
-      if (tok <= hi) bad += (rk.x != kL) + (rv.x != kL);
+      if (att) bad += (rk.x != kL || bad_k) + (rv.x != kL || bad_v);
 #ifdef DQ_CHECKED
       // The cursor starts at byte 5 and moves 32 per byte consumed.
-      if (tok <= hi)
+      if (att)
         over += (rk.p > static_cast<uint32_t>(kb - smem) + static_cast<uint32_t>(ck) * kGrp) +
                 (rv.p > static_cast<uint32_t>(vb - smem) + static_cast<uint32_t>(cv) * kGrp);
 #endif
@@ -615,6 +646,7 @@ __device__ __forceinline__ void wht_4(float (&z)[4]) {
   z[3] = __fsub_rn(a1, a3);
 }
 
+template <bool kWin>
 __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int ns = kMaxSlots;  // the host checks a.nslots against it
@@ -640,8 +672,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
   const int i_hi = min(i_lo + Mt, a.n_q) - 1;
   const int64_t lo_pos = max(qs + i_lo, int64_t(0));
   const int64_t hi_pos = min(qs + i_hi, a.T_cap - 1);
-  const int nB = lo_pos <= hi_pos ? static_cast<int>(hi_pos / kBlk) + 1 : 0;  // 128-token blocks to attend
-  const int64_t gslots = (a.T_cap + kBlk - 1) / kBlk;
+  // 128-token blocks to attend: block_at(j) is the j-th one's place in the cache.
+  int head = 0, skip = 0;
+  if constexpr (kWin) {
+    const WindowSpan sp = window_span(window_start(lo_pos, a.window), hi_pos + 1, a.sinks, kBlk);
+    head = static_cast<int>(sp.head);
+    skip = static_cast<int>(sp.skip);
+  }
+  auto block_at = [&](int j) { return kWin && j >= head ? j + skip : j; };
+  const int nB = lo_pos <= hi_pos ? static_cast<int>(hi_pos / kBlk) + 1 - skip : 0;
+  const int64_t gslots = kWin ? a.row_slots : (a.T_cap + kBlk - 1) / kBlk;
 
   // A softmax thread's query row (thread = row r of the block). Its loads
   // start before the set-up barrier, so that their latency overlaps the
@@ -746,10 +786,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
       if (amax > 0.0f && amax < INFINITY) {
         int ex;
         frexpf(amax, &ex);
-        sc = ldexpf(1.0f, 14 - ex);
+        sc = ldexpf(1.0f, min(14 - ex, 120));  // (finite for the smallest queries)
       }
       // logit (log2 units) = S * ||k|| * crow, with S = sum (q~ sc)(kappa_K y)
       crow = row_ok ? a.sm_scale * kLog2e / (static_cast<float>(kD) * sc * a.tabs->k.score_scale) : 0.0f;
+      // (A masked score is -inf times crow: crow must not underflow to 0.)
+      if constexpr (kWin) crow = row_ok ? fmaxf(crow, 1.17549435e-38f) : 0.0f;
       // Coordinates 32 m + 8 qt + 2 p, + 1 are packed fp16 column 16 m + 4 qt + p.
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -793,9 +835,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
         }
         // u = S ||k|| (the logit divided by crow > 0); tokens past this row's
         // position are masked, which only happens on the causal diagonal.
-        const int64_t rel = pos - static_cast<int64_t>(j) * kBlk - 32 * qt;
+        const int64_t tok0 = static_cast<int64_t>(block_at(j)) * kBlk + 32 * qt;
+        const int64_t rel = pos - tok0;
         const int lim = (!row_ok || rel < 0) ? -1 : (rel > 31 ? 31 : static_cast<int>(rel));
-        if (!__all_sync(kFull, lim >= 31)) {
+        if constexpr (kWin) {
+          // Also masked: tokens before the row's window that are not among
+          // the first `sinks` ones, i.e. sl <= t < wl.
+          const int64_t wr = rel - a.window + 1, sr = a.sinks - tok0;
+          const int wl = wr < 0 ? 0 : (wr > 32 ? 32 : static_cast<int>(wr));
+          const int sl = sr < 0 ? 0 : (sr > 32 ? 32 : static_cast<int>(sr));
+          if (!__all_sync(kFull, lim >= 31 && sl >= wl)) {
+#pragma unroll
+            for (int t = 0; t < 32; ++t) u[t] = t <= lim && (t >= wl || t < sl) ? u[t] : -INFINITY;
+          }
+        } else if (!__all_sync(kFull, lim >= 31)) {
 #pragma unroll
           for (int t = 0; t < 32; ++t) u[t] = t <= lim ? u[t] : -INFINITY;
         }
@@ -1099,6 +1152,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
     // ===== slot loader (one lane) =====
     if (lane == 0 && nB > 0) {
       const uint8_t *src = a.tiles + static_cast<size_t>((bh - a.bh0) * gslots) * kSlotBytes;
+      // Workspace slot of a block: the row's slots are those of the whole
+      // chunk, of which this CTA sees a part.
+      int64_t row_head = 0, row_skip = 0;
+      if constexpr (kWin) {
+        const WindowSpan sp = window_span(window_start(qs, a.window), last_position(qs, a.n_q, a.T_cap) + 1, a.sinks, kBlk);
+        row_head = sp.head;
+        row_skip = sp.skip;
+      }
+      auto slot_at = [&](int j) -> size_t {
+        const int64_t blk = block_at(j);
+        return static_cast<size_t>(kWin && blk >= row_head ? blk - row_skip : blk);
+      };
       int issued = 0;
       for (int j = 0; j < nB; ++j) {
         const int sl = static_cast<int>(j % ns);
@@ -1107,7 +1172,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
           break;
         }
         mbar_arrive_expect_tx(bars + kBarFull + sl, kSlotBytes);
-        bulk_g2s(slot_base(sl), src + static_cast<size_t>(j) * kSlotBytes, kSlotBytes, bars + kBarFull + sl);
+        bulk_g2s(slot_base(sl), src + slot_at(j) * kSlotBytes, kSlotBytes, bars + kBarFull + sl);
         ++issued;
       }
       // Drain: the last copies into each slot have landed before the CTA
@@ -1144,13 +1209,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
   }
 }
 
-template <bool kTwoK, bool kTwoV>
+template <bool kTwoK, bool kTwoV, bool kWin>
 int launch_tiles_t(const PrefillArgs &a, cudaStream_t st) {
   const TilesSmem L = tiles_smem_layout(a.ck, a.cv);
-  constexpr auto kern = prefill_tiles_kernel<kTwoK, kTwoV>;
+  constexpr auto kern = prefill_tiles_kernel<kTwoK, kTwoV, kWin>;
   const cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
   if (e != cudaSuccess) return static_cast<int>(e);
   kern<<<a.tile_grid, kTileWarps * 32, L.total, st>>>(a);
+  return static_cast<int>(cudaGetLastError());
+}
+
+// Tile and attention kernels of one wave.
+template <bool kWin>
+int launch_wave(const PrefillArgs &a, unsigned grid, cudaStream_t st) {
+  int e;
+  if (a.two_k && a.two_v) e = launch_tiles_t<true, true, kWin>(a, st);
+  else if (a.two_k) e = launch_tiles_t<true, false, kWin>(a, st);
+  else if (a.two_v) e = launch_tiles_t<false, true, kWin>(a, st);
+  else e = launch_tiles_t<false, false, kWin>(a, st);
+  if (e) return e;
+  const AttnSmem L = attn_smem_layout(a.nslots);
+  const cudaError_t ce = ensure_max_dynamic_smem<prefill_kernel<kWin>>(static_cast<int>(L.total));
+  if (ce != cudaSuccess) return static_cast<int>(ce);
+  prefill_kernel<kWin><<<grid, kAttnThreads, L.total, st>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -1167,9 +1248,15 @@ int64_t prefill_grid(int64_t nbh, int G, int n_q) {
   return nbh * ((n_q + Mt - 1) / Mt);
 }
 
-size_t prefill_workspace_bytes(int B, int Hkv, int64_t T_cap) {
-  return static_cast<size_t>(B) * Hkv * static_cast<size_t>((T_cap + kBlk - 1) / kBlk) * kSlotBytes;
+int64_t prefill_row_slots(int64_t T_cap, int n_q, int64_t window, int64_t sinks) {
+  const int64_t all = (T_cap + kBlk - 1) / kBlk;
+  if (window <= 0) return all;
+  // The chunk's windows cover at most window + n_q - 1 consecutive tokens.
+  const int64_t most = (sinks + kBlk - 1) / kBlk + (window + n_q - 1 + kBlk - 2) / kBlk + 1;
+  return most < all ? most : all;
 }
+
+size_t prefill_slot_bytes() { return kSlotBytes; }
 
 bool prefill_supported(int ck, int cv) {
   return ck >= 1 && cv >= 1 && ck <= kMaxContainer && cv <= kMaxContainer &&
@@ -1183,17 +1270,8 @@ int launch_prefill_attention(const PrefillArgs &a, void *stream) {
     return static_cast<int>(cudaErrorInvalidValue);
   const int64_t grid = prefill_grid(a.nbh, a.G, a.n_q);
   if (grid < 1 || grid > 0x7FFFFFFF) return static_cast<int>(cudaErrorInvalidValue);
-  int e;
-  if (a.two_k && a.two_v) e = launch_tiles_t<true, true>(a, st);
-  else if (a.two_k) e = launch_tiles_t<true, false>(a, st);
-  else if (a.two_v) e = launch_tiles_t<false, true>(a, st);
-  else e = launch_tiles_t<false, false>(a, st);
-  if (e) return e;
-  const AttnSmem L = attn_smem_layout(a.nslots);
-  const cudaError_t ce = ensure_max_dynamic_smem<prefill_kernel>(static_cast<int>(L.total));
-  if (ce != cudaSuccess) return static_cast<int>(ce);
-  prefill_kernel<<<static_cast<unsigned>(grid), kAttnThreads, L.total, st>>>(a);
-  return static_cast<int>(cudaGetLastError());
+  return a.window > 0 ? launch_wave<true>(a, static_cast<unsigned>(grid), st)
+                      : launch_wave<false>(a, static_cast<unsigned>(grid), st);
 }
 
 }  // namespace dqi

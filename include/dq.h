@@ -369,6 +369,60 @@ int dq_prefill_attention_paged(const dq_tables *t, const void *q, int q_dtype,
                                void *out, int out_dtype, void *d_workspace,
                                size_t ws_bytes, dq_stats *d_stats, void *stream);
 
+/* Attention with a sliding window and a few first tokens that stay visible.
+ * A query at position p sees cache token t when
+ *     t <= p  and  (t > p - window  or  t < sinks),
+ * so a sequence's cost no longer grows with its length: the containers (and,
+ * paged, the page-table entries) between the first tokens and the window are
+ * neither read nor decoded, and their pages may have been given back (see
+ * dq_pages_advance). The D-Quant pages describe no window; the decoding and
+ * the attention are those of the calls above.
+ *   window      tokens up to and including the query's own, >= 1
+ *   sinks       first tokens that every query sees, >= 0
+ *   sm_scale    must be positive
+ * Out of range arguments give DQ_ERR_SHAPE. With window >= T_cap the result is
+ * that of the call without a window. A container whose fp16 norm is infinite
+ * or NaN (a corrupt one) counts in integrity_errors and its norm as 0, so it
+ * cannot reach the queries that do not see it. Everything else is as in
+ * dq_decode_attention[_paged] (p = length - 1; the workspace is
+ * dq_decode_workspace_bytes, length 0 gives out = 0) and in
+ * dq_prefill_attention[_paged] (p = d_q_start[b] + i). The prefill workspace
+ * holds the decoded tiles of what a chunk sees: dq_prefill_window_workspace_
+ * bytes(...) for the whole batch, at least that of one (b, KV head) row. */
+int dq_decode_attention_window(const dq_tables *t, const void *q, int q_dtype,
+                               const uint8_t *d_kcache, const uint8_t *d_vcache,
+                               const int32_t *d_seq_lens, int B, int Hq, int Hkv,
+                               int64_t T_cap, int64_t T_max, int64_t window,
+                               int64_t sinks, float sm_scale, void *out,
+                               int out_dtype, void *d_workspace, size_t ws_bytes,
+                               dq_stats *d_stats, void *stream);
+int dq_decode_attention_window_paged(const dq_tables *t, const void *q, int q_dtype,
+                                     const uint8_t *d_kpool, const uint8_t *d_vpool,
+                                     int64_t num_pages, const int32_t *d_page_table,
+                                     int64_t max_pages, const int32_t *d_seq_lens,
+                                     int B, int Hq, int Hkv, int64_t T_max,
+                                     int64_t window, int64_t sinks, float sm_scale,
+                                     void *out, int out_dtype, void *d_workspace,
+                                     size_t ws_bytes, dq_stats *d_stats, void *stream);
+size_t dq_prefill_window_workspace_bytes(const dq_tables *t, int B, int Hkv,
+                                         int64_t T_cap, int n_q, int64_t window,
+                                         int64_t sinks);
+int dq_prefill_attention_window(const dq_tables *t, const void *q, int q_dtype,
+                                const uint8_t *d_kcache, const uint8_t *d_vcache,
+                                const int32_t *d_q_start, int B, int n_q, int Hq,
+                                int Hkv, int64_t T_cap, int64_t window,
+                                int64_t sinks, float sm_scale, void *out,
+                                int out_dtype, void *d_workspace, size_t ws_bytes,
+                                dq_stats *d_stats, void *stream);
+int dq_prefill_attention_window_paged(const dq_tables *t, const void *q, int q_dtype,
+                                      const uint8_t *d_kpool, const uint8_t *d_vpool,
+                                      int64_t num_pages, const int32_t *d_page_table,
+                                      int64_t max_pages, const int32_t *d_q_start,
+                                      int B, int n_q, int Hq, int Hkv, int64_t window,
+                                      int64_t sinks, float sm_scale, void *out,
+                                      int out_dtype, void *d_workspace, size_t ws_bytes,
+                                      dq_stats *d_stats, void *stream);
+
 /* Test hook: decodes n flat containers of one stream.
  *   d_cache   device [n][C]; d_syms device uint8 [n][128]; d_norm16 device
  *             uint16 [n]; d_status device int32 [n] (may be NULL)
