@@ -16,6 +16,8 @@ from ._native import (DQ_BF16, DQ_F32, DQ_STREAM_K, DQ_STREAM_V, DqConfig, DqErr
                       dq_prefill_workspace_bytes, dq_decode_attention_window, dq_decode_attention_window_paged,
                       dq_prefill_attention_window, dq_prefill_attention_window_paged,
                       dq_prefill_window_workspace_bytes,
+                      dq_pages_advance, dq_pages_compact, dq_pages_copy, dq_pages_fork, dq_pages_workspace_bytes,
+                      new_page_counts, new_page_state, page_counts_dict,
                       new_pool,
                       dq_decode_symbols, dq_decode_workspace_bytes,
                       dq_design_stream, dq_error_string, load, new_cache, new_stats,

@@ -30,7 +30,9 @@ EXPORTED = ("dq_config_default", "dq_build_tables", "dq_free_tables", "dq_get_st
             "dq_append_kv_ws", "dq_append_kv_paged", "dq_decode_attention_paged",
             "dq_prefill_attention", "dq_prefill_attention_paged", "dq_prefill_workspace_bytes",
             "dq_decode_attention_window", "dq_decode_attention_window_paged", "dq_prefill_attention_window",
-            "dq_prefill_attention_window_paged", "dq_prefill_window_workspace_bytes")
+            "dq_prefill_attention_window_paged", "dq_prefill_window_workspace_bytes",
+            "dq_pages_workspace_bytes", "dq_pages_advance", "dq_pages_fork", "dq_pages_compact", "dq_pages_copy")
+PAGE_COUNT_FIELDS = ("free_pages", "taken", "released", "short_of", "bad", "clamped", "pairs", "reserved")
 
 
 class DqConfig(C.Structure):
@@ -111,6 +113,12 @@ def load():
     lib.dq_prefill_attention_window_paged.argtypes = [vp, vp, C.c_int, vp, vp, i64, vp, i64, vp, C.c_int, C.c_int,
                                                       C.c_int, C.c_int, i64, i64, C.c_float, vp, C.c_int, vp,
                                                       C.c_size_t, vp, vp]
+    lib.dq_pages_workspace_bytes.argtypes = [vp, i64, C.c_int, i64]
+    lib.dq_pages_workspace_bytes.restype = C.c_size_t
+    lib.dq_pages_advance.argtypes = [vp, i64, vp, vp, i64, vp, vp, C.c_int, i64, i64, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.dq_pages_fork.argtypes = [vp, i64, vp, vp, i64, vp, C.c_int, vp, C.c_int, vp, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.dq_pages_compact.argtypes = [vp, i64, vp, vp, i64, C.c_int, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.dq_pages_copy.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp]
     lib.dq_error_string.argtypes = [C.c_int]
     lib.dq_error_string.restype = C.c_char_p
     lib.dq_last_cuda_error.argtypes = []
@@ -494,6 +502,121 @@ def dq_prefill_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch
         page_table.shape[1], _ptr(q_start), B, n_q, Hq, kpool.shape[1], window, sinks,
         float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(stats), _stream(stream)))
+
+
+def new_page_state(num_pages: int, B: int, max_pages: int, device=None):
+    """(refs [num_pages], page_table [B, max_pages], lens [B]) of an empty paged cache, int32."""
+    device = device or "cuda"
+    return (torch.zeros(num_pages, dtype=torch.int32, device=device),
+            torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+            torch.zeros(B, dtype=torch.int32, device=device))
+
+
+def new_page_counts(device=None) -> torch.Tensor:
+    """A zeroed device dq_page_counts (one int32 per field of PAGE_COUNT_FIELDS)."""
+    return torch.zeros(len(PAGE_COUNT_FIELDS), dtype=torch.int32, device=device or "cuda")
+
+
+def page_counts_dict(counts: torch.Tensor) -> dict:
+    return dict(zip(PAGE_COUNT_FIELDS, counts.cpu().tolist()))
+
+
+def _check_int32(**tensors) -> None:
+    """Name = (tensor, shape): an int32 tensor of that shape."""
+    for name, (t, shape) in tensors.items():
+        if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must be int32 %s, got %s %s" % (name, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+def dq_pages_workspace_bytes(tab: Tables, num_pages: int, B: int, max_pages: int) -> int:
+    """Bytes of the workspace of dq_pages_advance, _fork and _compact for tables of at most B rows."""
+    return int(load().dq_pages_workspace_bytes(tab.handle, num_pages, B, max_pages))
+
+
+def dq_pages_advance(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                     n_new: torch.Tensor, refs_out: torch.Tensor, page_table_out: torch.Tensor,
+                     lens_out: torch.Tensor, counts: torch.Tensor, workspace: torch.Tensor, window: int = 0,
+                     sinks: int = 0, stream=None) -> None:
+    """The pages of the next n_new[b] tokens of every sequence (n_new[b] < 0:
+    the sequence ends); with a window the pages behind it go back. int32: refs
+    [num_pages], page_table [B, max_pages], lens and n_new [B]; the outputs may
+    be the inputs."""
+    _check_cuda(refs=refs, page_table=page_table, lens=lens, n_new=n_new, refs_out=refs_out,
+                page_table_out=page_table_out, lens_out=lens_out, counts=counts, workspace=workspace)
+    B, max_pages = page_table.shape
+    P = refs.numel()
+    _check_int32(refs=(refs, (P,)), page_table=(page_table, (B, max_pages)), lens=(lens, (B,)), n_new=(n_new, (B,)),
+                 refs_out=(refs_out, (P,)), page_table_out=(page_table_out, (B, max_pages)),
+                 lens_out=(lens_out, (B,)), counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check("dq_pages_advance", load().dq_pages_advance(
+        tab.handle, P, _ptr(refs), _ptr(page_table), max_pages, _ptr(lens), _ptr(n_new), B, window, sinks,
+        _ptr(refs_out), _ptr(page_table_out), _ptr(lens_out), _ptr(counts), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def dq_pages_fork(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                  parent: torch.Tensor, refs_out: torch.Tensor, page_table_out: torch.Tensor,
+                  lens_out: torch.Tensor, pairs: torch.Tensor, counts: torch.Tensor, workspace: torch.Tensor,
+                  stream=None) -> None:
+    """Row c of the new table [B_out, max_pages] is row parent[c] of the old
+    one (negative: empty). Pages are shared; pairs [B_out, 2] lists the copies
+    of partly filled last pages for dq_pages_copy. Outputs must be other
+    tensors than the inputs."""
+    _check_cuda(refs=refs, page_table=page_table, lens=lens, parent=parent, refs_out=refs_out,
+                page_table_out=page_table_out, lens_out=lens_out, pairs=pairs, counts=counts, workspace=workspace)
+    B, max_pages = page_table.shape
+    P, B_out = refs.numel(), parent.numel()
+    _check_int32(refs=(refs, (P,)), page_table=(page_table, (B, max_pages)), lens=(lens, (B,)),
+                 parent=(parent, (B_out,)), refs_out=(refs_out, (P,)),
+                 page_table_out=(page_table_out, (B_out, max_pages)), lens_out=(lens_out, (B_out,)),
+                 pairs=(pairs, (B_out, 2)), counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check("dq_pages_fork", load().dq_pages_fork(
+        tab.handle, P, _ptr(refs), _ptr(page_table), max_pages, _ptr(lens), B, _ptr(parent), B_out, _ptr(refs_out),
+        _ptr(page_table_out), _ptr(lens_out), _ptr(pairs), _ptr(counts), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def dq_pages_compact(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, refs_out: torch.Tensor,
+                     page_table_out: torch.Tensor, pairs: torch.Tensor, counts: torch.Tensor,
+                     workspace: torch.Tensor, stream=None) -> None:
+    """Renumbers the pages in use to the lowest numbers; pairs [max(1,
+    num_pages // 2), 2] lists the moves for dq_pages_copy. The outputs may be
+    the inputs."""
+    _check_cuda(refs=refs, page_table=page_table, refs_out=refs_out, page_table_out=page_table_out, pairs=pairs,
+                counts=counts, workspace=workspace)
+    B, max_pages = page_table.shape
+    P = refs.numel()
+    _check_int32(refs=(refs, (P,)), page_table=(page_table, (B, max_pages)), refs_out=(refs_out, (P,)),
+                 page_table_out=(page_table_out, (B, max_pages)), pairs=(pairs, (max(1, P // 2), 2)),
+                 counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check("dq_pages_compact", load().dq_pages_compact(
+        tab.handle, P, _ptr(refs), _ptr(page_table), max_pages, B, _ptr(refs_out), _ptr(page_table_out), _ptr(pairs),
+        _ptr(counts), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def dq_pages_copy(tab: Tables, kpool: torch.Tensor, vpool: torch.Tensor, pairs: torch.Tensor,
+                  counts: torch.Tensor | None = None, stats: torch.Tensor | None = None, stream=None) -> None:
+    """Copies the pages that pairs int32 [n, 2] names (source, destination) in
+    pools [num_pages, Hkv, C, 32], or [layers, num_pages, Hkv, C, 32] (each
+    layer contiguous): the first counts.pairs of them, or all."""
+    _check_cuda(pairs=pairs, counts=counts, stats=stats)
+    kl, vl = (p if p.dim() == 5 else p.unsqueeze(0) for p in (kpool, vpool))
+    if kl.dim() != 5 or vl.dim() != 5 or kl.shape[0] != vl.shape[0]:
+        raise ValueError("pools must have 4 dimensions, or 5 with as many layers, got %s and %s"
+                         % (tuple(kpool.shape), tuple(vpool.shape)))
+    if kl.shape[0] == 0:
+        return
+    _check_cuda(kpool=kl[0], vpool=vl[0], pairs=pairs)
+    for name, p, s in (("kpool", kl, tab.k), ("vpool", vl, tab.v)):
+        want = (kl.shape[1], tab.n_kv_heads, s.container_bytes, 32)
+        if p.dtype != torch.uint8 or tuple(p.shape[1:]) != want:
+            raise ValueError("%s must be uint8 %s in each layer, got %s %s" % (name, want, p.dtype, tuple(p.shape)))
+    _check_int32(pairs=(pairs, (pairs.shape[0], 2)))
+    if counts is not None:
+        _check_int32(counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check("dq_pages_copy", load().dq_pages_copy(
+        tab.handle, _ptr(kl), _ptr(vl), kl.shape[1], kl.shape[0], kl.stride(0), vl.stride(0), _ptr(pairs),
+        pairs.shape[0], _ptr(counts), _ptr(stats), _stream(stream)))
 
 
 def dq_decode_symbols(tab: Tables, cache: torch.Tensor, kind: int, syms: torch.Tensor,

@@ -170,6 +170,9 @@ struct WsLayout {
   size_t prefix_off = 0, o_off = 0, ml_off = 0, total = 0;
 };
 
+// Pages of a row in the bookkeeping calls: its tokens are counted in int32.
+constexpr int64_t kMaxTablePages = int64_t(1) << 26;
+
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 WsLayout ws_layout(const dq_tables *t, int B, int Hkv, int G) {
@@ -698,6 +701,150 @@ int dq_prefill_attention_window_paged(const dq_tables *t, const void *q, int q_d
   return prefill_core(t, q, q_dtype, d_kpool, d_vpool, d_q_start, B, n_q, Hq, Hkv, 32 * max_pages, sm_scale, out,
                       out_dtype, d_workspace, ws_bytes, d_stats, stream, d_page_table, max_pages, num_pages, window,
                       sinks);
+}
+
+size_t dq_pages_workspace_bytes(const dq_tables *t, int64_t num_pages, int B, int64_t max_pages) {
+  if (!t || num_pages < 1 || num_pages > 0x7FFFFFFF || B < 0 || max_pages < 1 || max_pages > kMaxTablePages) return 0;
+  return dqi::pages_layout(num_pages, B, max_pages).total;
+}
+
+// Checks and arguments that the bookkeeping calls share; rows of the old and
+// the new table. Arrays of no rows may be NULL.
+static int pages_args(const dq_tables *t, int64_t num_pages, int64_t max_pages, const int32_t *d_refs,
+                      const int32_t *d_table, int B_in, int32_t *d_refs_out, int32_t *d_table_out, int B_out,
+                      int32_t *d_counts, void *d_workspace, size_t ws_bytes, dqi::PagesArgs *a) {
+  if (!t || !d_refs || !d_refs_out || !d_counts || !d_workspace || (B_in > 0 && !d_table) || (B_out > 0 && !d_table_out))
+    return DQ_ERR_NULL;
+  if (num_pages < 1 || num_pages > 0x7FFFFFFF || max_pages < 1 || max_pages > kMaxTablePages || B_in < 0 || B_out < 0)
+    return DQ_ERR_SHAPE;
+  if (!aligned(d_refs, 4) || !aligned(d_table, 4) || !aligned(d_refs_out, 4) || !aligned(d_table_out, 4) ||
+      !aligned(d_counts, 4) || !aligned(d_workspace, 16))
+    return DQ_ERR_ALIGN;
+  const dqi::PagesLayout l = dqi::pages_layout(num_pages, std::max(B_in, B_out), max_pages);
+  if (ws_bytes < l.total) return DQ_ERR_WORKSPACE;
+  const int rc = check_device(t);
+  if (rc != DQ_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(d_workspace);
+  auto at = [&](size_t off) { return reinterpret_cast<int32_t *>(ws + off); };
+  *a = dqi::PagesArgs{};
+  a->num_pages = num_pages;
+  a->max_pages = max_pages;
+  a->B_in = B_in;
+  a->B_out = B_out;
+  a->refs_in = d_refs;
+  a->table_in = d_table;
+  a->refs_out = d_refs_out;
+  a->table_out = d_table_out;
+  a->counts = d_counts;
+  a->list = at(l.list);
+  a->item_need = at(l.need);
+  a->item_lo = at(l.lo);
+  a->item_hi = at(l.hi);
+  a->map = a->children = at(l.map);
+  a->movers = a->first = at(l.movers);
+  return DQ_OK;
+}
+
+int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_refs, const int32_t *d_page_table,
+                     int64_t max_pages, const int32_t *d_lens, const int32_t *d_n_new, int B, int64_t window,
+                     int64_t sinks, int32_t *d_refs_out, int32_t *d_page_table_out, int32_t *d_lens_out,
+                     dq_page_counts *d_counts, void *d_workspace, size_t ws_bytes, void *stream) {
+  try {
+    if (B > 0 && (!d_lens || !d_n_new || !d_lens_out)) return DQ_ERR_NULL;
+    if (window < 0 || sinks < 0) return DQ_ERR_SHAPE;
+    if (!aligned(d_lens, 4) || !aligned(d_n_new, 4) || !aligned(d_lens_out, 4)) return DQ_ERR_ALIGN;
+    dqi::PagesArgs a;
+    const int rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B, d_refs_out, d_page_table_out, B,
+                              reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
+    if (rc != DQ_OK) return rc;
+    a.lens_in = d_lens;
+    a.step = d_n_new;
+    a.lens_out = d_lens_out;
+    a.window = std::min<int64_t>(window, int64_t(1) << 40);  // (any length is below)
+    a.sinks = std::min<int64_t>(sinks, int64_t(1) << 40);
+    const int e = dqi::launch_pages_advance(a, stream);
+    return e == 0 ? DQ_OK : cuda_fail(static_cast<cudaError_t>(e));
+  } catch (...) {
+    return DQ_ERR_CUDA;
+  }
+}
+
+int dq_pages_fork(const dq_tables *t, int64_t num_pages, const int32_t *d_refs, const int32_t *d_page_table,
+                  int64_t max_pages, const int32_t *d_lens, int B_in, const int32_t *d_parent, int B_out,
+                  int32_t *d_refs_out, int32_t *d_page_table_out, int32_t *d_lens_out, int32_t *d_pairs,
+                  dq_page_counts *d_counts, void *d_workspace, size_t ws_bytes, void *stream) {
+  try {
+    if ((B_in > 0 && !d_lens) || (B_out > 0 && (!d_parent || !d_lens_out || !d_pairs))) return DQ_ERR_NULL;
+    if (!aligned(d_lens, 4) || !aligned(d_parent, 4) || !aligned(d_lens_out, 4) || !aligned(d_pairs, 4))
+      return DQ_ERR_ALIGN;
+    // The new rows are read from the old ones in any order.
+    if (d_refs && d_refs == d_refs_out) return DQ_ERR_SHAPE;
+    if (B_in > 0 && B_out > 0 && (d_page_table == d_page_table_out || d_lens == d_lens_out)) return DQ_ERR_SHAPE;
+    dqi::PagesArgs a;
+    const int rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B_in, d_refs_out, d_page_table_out, B_out,
+                              reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
+    if (rc != DQ_OK) return rc;
+    a.lens_in = d_lens;
+    a.step = d_parent;
+    a.lens_out = d_lens_out;
+    a.pairs = d_pairs;
+    const int e = dqi::launch_pages_fork(a, stream);
+    return e == 0 ? DQ_OK : cuda_fail(static_cast<cudaError_t>(e));
+  } catch (...) {
+    return DQ_ERR_CUDA;
+  }
+}
+
+int dq_pages_compact(const dq_tables *t, int64_t num_pages, const int32_t *d_refs, const int32_t *d_page_table,
+                     int64_t max_pages, int B, int32_t *d_refs_out, int32_t *d_page_table_out, int32_t *d_pairs,
+                     dq_page_counts *d_counts, void *d_workspace, size_t ws_bytes, void *stream) {
+  try {
+    if (!d_pairs) return DQ_ERR_NULL;
+    if (!aligned(d_pairs, 4)) return DQ_ERR_ALIGN;
+    dqi::PagesArgs a;
+    const int rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B, d_refs_out, d_page_table_out, B,
+                              reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
+    if (rc != DQ_OK) return rc;
+    a.pairs = d_pairs;
+    const int e = dqi::launch_pages_compact(a, stream);
+    return e == 0 ? DQ_OK : cuda_fail(static_cast<cudaError_t>(e));
+  } catch (...) {
+    return DQ_ERR_CUDA;
+  }
+}
+
+int dq_pages_copy(const dq_tables *t, uint8_t *d_kpool, uint8_t *d_vpool, int64_t num_pages, int64_t n_layers,
+                  int64_t k_layer_stride, int64_t v_layer_stride, const int32_t *d_pairs, int64_t max_pairs,
+                  const dq_page_counts *d_counts, dq_stats *d_stats, void *stream) {
+  try {
+    if (!t || !d_kpool || !d_vpool || (max_pairs > 0 && !d_pairs)) return DQ_ERR_NULL;
+    if (num_pages < 1 || num_pages > (int64_t(1) << 31) || n_layers < 0 || n_layers > (1 << 20) || max_pairs < 0 ||
+        max_pairs > (int64_t(1) << 31))
+      return DQ_ERR_SHAPE;
+    if (!aligned(d_kpool, 16) || !aligned(d_vpool, 16) || k_layer_stride % 16 || v_layer_stride % 16 ||
+        !aligned(d_pairs, 4) || !aligned(d_counts, 4))
+      return DQ_ERR_ALIGN;
+    const int rc = check_device(t);
+    if (rc != DQ_OK) return rc;
+    if (n_layers == 0 || max_pairs == 0) return DQ_OK;
+    dqi::CopyArgs a{};
+    a.kpool = d_kpool;
+    a.vpool = d_vpool;
+    a.num_pages = num_pages;
+    a.n_layers = n_layers;
+    a.k_stride = k_layer_stride;
+    a.v_stride = v_layer_stride;
+    a.k_bytes = static_cast<int64_t>(t->cfg.n_kv_heads) * 32 * t->k.container_bytes;
+    a.v_bytes = static_cast<int64_t>(t->cfg.n_kv_heads) * 32 * t->v.container_bytes;
+    a.pairs = d_pairs;
+    a.max_pairs = max_pairs;
+    a.counts = reinterpret_cast<const int32_t *>(d_counts);
+    a.stats = d_stats;
+    const int e = dqi::launch_pages_copy(a, t->sm_count, stream);
+    return e == 0 ? DQ_OK : cuda_fail(static_cast<cudaError_t>(e));
+  } catch (...) {
+    return DQ_ERR_CUDA;
+  }
 }
 
 int dq_decode_symbols(const dq_tables *t, const uint8_t *d_cache, int stream_kind,

@@ -92,6 +92,22 @@ cudaError_t ensure_max_dynamic_smem(int bytes) {
   return e;
 }
 
+// Lets kernel Kern be launched in clusters of more than 8 CTAs on the current
+// device; the attribute call is made once per device, as above.
+template <auto Kern>
+cudaError_t allow_wide_cluster() {
+  constexpr int kDevs = 64;
+  static std::atomic<bool> set[kDevs];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < kDevs;
+  if (cached && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && cached) set[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 // What a sliding window leaves of a run of blocks: the blocks that hold the
 // first tokens, then, `skip` blocks further, the blocks from the window's
 // first token to the last one. Visible block j is block j (j < head) or

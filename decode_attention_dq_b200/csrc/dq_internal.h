@@ -170,6 +170,42 @@ int64_t prefill_row_slots(int64_t T_cap, int n_q, int64_t window, int64_t sinks)
 size_t prefill_slot_bytes();
 bool prefill_supported(int ck, int cv);
 
+// Page bookkeeping and copies (dq_pages.cu).
+struct PagesArgs {
+  int64_t num_pages, max_pages;
+  int B_in, B_out;
+  const int32_t *refs_in, *table_in, *lens_in;
+  const int32_t *step;  // advance: new tokens of each row; fork: parent of each new row
+  int32_t *refs_out, *table_out, *lens_out;
+  int32_t *pairs;       // [][2] source and destination page of each copy, then -1
+  int32_t *counts;      // dq_page_counts
+  int64_t window, sinks;
+  // Workspace (pages_layout).
+  int32_t *list;        // pages in the order in which they are handed out or filled
+  int32_t *item_need, *item_lo, *item_hi;
+  int32_t *map, *movers;
+  int32_t *children, *first;
+};
+// Offsets of the workspace's parts, in bytes.
+struct PagesLayout {
+  size_t list, need, lo, hi, map, movers, total;
+};
+PagesLayout pages_layout(int64_t num_pages, int64_t B, int64_t max_pages);
+int launch_pages_advance(const PagesArgs &a, void *stream);
+int launch_pages_fork(const PagesArgs &a, void *stream);
+int launch_pages_compact(const PagesArgs &a, void *stream);
+
+struct CopyArgs {
+  uint8_t *kpool, *vpool;
+  int64_t num_pages, n_layers, k_stride, v_stride;  // bytes from one layer's pool to the next
+  int64_t k_bytes, v_bytes;                         // of a page
+  const int32_t *pairs;
+  int64_t max_pairs;
+  const int32_t *counts;  // dq_page_counts, or nullptr: all pairs
+  dq_stats *stats;
+};
+int launch_pages_copy(const CopyArgs &a, int sm_count, void *stream);
+
 struct SymbolsArgs {
   const DevStream *tab;
   const uint8_t *cache;

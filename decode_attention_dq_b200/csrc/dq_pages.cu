@@ -1,0 +1,640 @@
+// dq_pages.cu -- the pages of a paged cache: advancing every sequence by a
+// step, forking sequences, compacting a pool, and copying pages.
+//
+// The state is three arrays of whole numbers: refs[p], how many references
+// page p has (0: free), the page table T[b][j] (-1: no page) and the lengths
+// L[b]. Each bookkeeping call reads one state and writes the next one:
+//   advance  gives back what a sequence no longer needs and hands out the
+//            pages of its next tokens
+//   fork     row c of the new table is row parent[c] of the old one; full
+//            pages are shared, a partly filled last page is copied
+//   compact  moves the live pages to the lowest numbers
+// Pages are handed out lowest first, in the order of the rows, and holes are
+// filled in ascending order, so every result is determined by the state:
+// nothing depends on the order of the atomics (sums of whole numbers).
+//
+// One launch each: a cluster of kCluster CTAs goes through the phases with
+// hardware cluster barriers in between and exchanges its counts through
+// distributed shared memory. What bounds such a call at serving sizes is the
+// chain of phases (releases before the free pages are known, these before a
+// page is handed out), not bytes, and a barrier of one cluster costs less
+// than a kernel boundary.
+//
+// Free pages and holes are found in two passes over refs: each warp counts in
+// its own contiguous part, the counts are summed over the warps before it
+// (block scan) and the CTAs before (distributed shared memory), then the
+// warp goes through its part again and knows the rank of each page it finds.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "dq_device.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace dqi {
+namespace {
+
+constexpr int kCluster = 16;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSeg = 512;   // table entries that a warp handles at a time (a work item)
+constexpr int kPage = 32;   // tokens per page
+constexpr int kUnroll = 8;  // loads in flight per lane
+
+// A CTA's part of the counts that the cluster exchanges.
+struct Totals {
+  long long free_pages, need;
+  int released, bad, clamped, gained;  // gained: pages that became free less pages that ceased to be
+};
+
+// Sum of v over the warps of the CTA below this one and over all of them;
+// the same for every lane of a warp. Two barriers.
+__device__ __forceinline__ long long block_exclusive(long long v, long long *sh, long long &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) sh[warp] = v;
+  __syncthreads();
+  long long x = sh[lane], before = lane < warp ? x : 0;
+  for (int o = 16; o; o >>= 1) {
+    x += __shfl_xor_sync(kFull, x, o);
+    before += __shfl_xor_sync(kFull, before, o);
+  }
+  total = x;
+  return before;
+}
+
+// [lo, hi) of part i out of n of [0, size).
+__device__ __forceinline__ void part(long long size, long long i, long long n, long long &lo, long long &hi) {
+  lo = size * i / n;
+  hi = size * (i + 1) / n;
+}
+
+// Calls f(index, value) in ascending rounds of 32 for refs[lo..hi): all lanes
+// call it, with a value of `other` for an index past the end.
+template <class F>
+__device__ __forceinline__ void for_refs(const int32_t *refs, long long lo, long long hi, int other, F f) {
+  const int lane = threadIdx.x & 31;
+  for (long long i0 = lo; i0 < hi; i0 += 32 * kUnroll) {
+    int v[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const long long i = i0 + 32 * k + lane;
+      v[k] = i < hi ? __ldcg(refs + i) : other;
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (i0 + 32 * k < hi) f(i0 + 32 * k + lane, v[k]);
+  }
+}
+
+__device__ __forceinline__ int ballot_rank(unsigned mask) {
+  return __popc(mask & ((1u << (threadIdx.x & 31)) - 1u));
+}
+
+__device__ __forceinline__ long long clamp_tokens(int len, long long cap) {
+  return len < 0 ? 0 : (len > cap ? cap : len);
+}
+
+// Adds a thread's counts to the CTA's.
+__device__ __forceinline__ void add_counts(Totals *mine, int released, int bad, int clamped, int gained) {
+  released = __reduce_add_sync(kFull, released);
+  bad = __reduce_add_sync(kFull, bad);
+  clamped = __reduce_add_sync(kFull, clamped);
+  gained = __reduce_add_sync(kFull, gained);
+  if ((threadIdx.x & 31) == 0) {
+    if (released) atomicAdd(&mine->released, released);
+    if (bad) atomicAdd(&mine->bad, bad);
+    if (clamped) atomicAdd(&mine->clamped, clamped);
+    if (gained) atomicAdd(&mine->gained, gained);
+  }
+}
+
+struct Shared {
+  Totals totals, before, all;
+  long long scan[kWarps];
+};
+
+// After a cluster barrier: the counts of the CTAs before this one (free pages
+// and needs) and of all. The first warp reads them, a CTA per lane.
+__device__ __forceinline__ void exchange(cg::cluster_group &cl, Shared &sh, Totals &before, Totals &all) {
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, rank = static_cast<int>(cl.block_rank());
+    Totals t{};
+    if (lane < kCluster) t = *cl.map_shared_rank(&sh.totals, lane);
+    Totals b{};
+    if (lane < rank) {
+      b.free_pages = t.free_pages;
+      b.need = t.need;
+    }
+    for (int o = 16; o; o >>= 1) {
+      b.free_pages += __shfl_xor_sync(kFull, b.free_pages, o);
+      b.need += __shfl_xor_sync(kFull, b.need, o);
+      t.free_pages += __shfl_xor_sync(kFull, t.free_pages, o);
+      t.need += __shfl_xor_sync(kFull, t.need, o);
+    }
+    t.released = __reduce_add_sync(kFull, t.released);
+    t.bad = __reduce_add_sync(kFull, t.bad);
+    t.clamped = __reduce_add_sync(kFull, t.clamped);
+    t.gained = __reduce_add_sync(kFull, t.gained);
+    if (lane == 0) {
+      sh.before = b;
+      sh.all = t;
+    }
+  }
+  __syncthreads();
+  before = sh.before;
+  all = sh.all;
+}
+
+// d_counts: see dq_page_counts in dq.h.
+__device__ __forceinline__ void write_counts(int32_t *c, long long free_pages, long long taken, int released,
+                                             long long short_of, int bad, int clamped, long long pairs) {
+  c[0] = static_cast<int32_t>(free_pages);
+  c[1] = static_cast<int32_t>(taken);
+  c[2] = released;
+  c[3] = static_cast<int32_t>(short_of);
+  c[4] = bad;
+  c[5] = clamped;
+  c[6] = static_cast<int32_t>(pairs);
+  c[7] = 0;
+}
+
+// The free pages (0 in `refs`) of this warp's part get their ranks; those
+// below `take` go into list[rank] and are taken in refs_out.
+__device__ __forceinline__ void list_free(const int32_t *refs, long long lo, long long hi, long long rank,
+                                          long long take, int32_t *list, int32_t *refs_out) {
+  if (rank >= take) return;
+  for_refs(refs, lo, hi, 1, [&](long long p, int v) {
+    const unsigned m = __ballot_sync(kFull, v == 0);
+    if (v == 0) {
+      const long long r = rank + ballot_rank(m);
+      if (r < take) {
+        list[r] = static_cast<int32_t>(p);
+        atomicAdd(refs_out + p, 1);
+      }
+    }
+    rank += __popc(m);
+  });
+}
+
+__device__ __forceinline__ long long count_free(const int32_t *refs, long long lo, long long hi) {
+  long long n = 0;
+  for_refs(refs, lo, hi, 1, [&](long long, int v) { n += __popc(__ballot_sync(kFull, v == 0)); });
+  return n;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) advance_kernel(const PagesArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cl.block_rank());
+  const long long P = a.num_pages, mp = a.max_pages, cap = kPage * mp < 0x7FFFFFFF ? kPage * mp : 0x7FFFFFFF;
+  const long long nseg = (mp + kSeg - 1) / kSeg, items = a.B_in * nseg;
+  if (threadIdx.x == 0) sh.totals = Totals{};
+  long long r_lo, r_hi, w_lo, w_hi, i_lo, i_hi;
+  part(P, rank, kCluster, r_lo, r_hi);
+  part(r_hi - r_lo, warp, kWarps, w_lo, w_hi);
+  w_lo += r_lo;
+  w_hi += r_lo;
+  part(items, rank, kCluster, i_lo, i_hi);
+  if (a.refs_out != a.refs_in)
+    for_refs(a.refs_in, w_lo, w_hi, 0, [&](long long p, int v) {
+      if (p < w_hi) a.refs_out[p] = v;
+    });
+  cl.sync();
+
+  // Rows: what is given back, and how many entries of each item want a page.
+  int released = 0, bad = 0, clamped = 0;
+  for (long long it = i_lo + warp; it < i_hi; it += kWarps) {
+    const long long b = it / nseg, j0 = (it % nseg) * kSeg, j1 = j0 + kSeg < mp ? j0 + kSeg : mp;
+    const int raw = a.lens_in[b], n = a.step[b];
+    const long long len = clamp_tokens(raw, cap), want = n < 0 ? 0 : len + n;
+    const long long len2 = want < cap ? want : cap;
+    if (j0 == 0 && lane == 0) clamped += (raw != len || want != len2) ? 1 : 0;
+    // Blocks [g_lo, g_hi) are given back; blocks [t_lo, t_hi) need a page.
+    long long g_lo = 0, g_hi = n < 0 ? mp : 0;
+    if (n >= 0 && a.window > 0) {
+      g_lo = (a.sinks + kPage - 1) / kPage;
+      const long long seen = len + 1 - a.window;  // the first token that a next one sees
+      g_hi = seen > 0 ? seen / kPage : 0;
+    }
+    const long long t_lo = n < 0 ? 0 : len / kPage, t_hi = n < 0 ? 0 : (len2 + kPage - 1) / kPage;
+    const int32_t *in = a.table_in + b * mp;
+    int32_t *out = a.table_out + b * mp;
+    int need = 0;
+    for (long long c0 = j0; c0 < j1; c0 += 32 * kUnroll) {
+      int e[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const long long j = c0 + 32 * k + lane;
+        e[k] = j < j1 ? in[j] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const long long j = c0 + 32 * k + lane;
+        if (j >= j1) continue;
+        const bool held = e[k] >= 0 && e[k] < P;
+        bad += (!held && e[k] != -1) ? 1 : 0;
+        const bool gone = j >= g_lo && j < g_hi;
+        if (held && gone) {
+          atomicSub(a.refs_out + e[k], 1);
+          ++released;
+        }
+        const int v = held && !gone ? e[k] : -1;
+        need += (v < 0 && j >= t_lo && j < t_hi) ? 1 : 0;
+        out[j] = v;
+      }
+    }
+    need = __reduce_add_sync(kFull, need);
+    if (lane == 0) {
+      a.item_need[it] = need;
+      a.item_lo[it] = static_cast<int32_t>(t_lo > j0 ? t_lo : j0);
+      a.item_hi[it] = static_cast<int32_t>(t_hi < j1 ? t_hi : j1);
+    }
+  }
+  add_counts(&sh.totals, released, bad, clamped, 0);
+  cl.sync();
+
+  // Lengths (all have been read); needs of this CTA; free pages of its part.
+  for (long long b = static_cast<long long>(rank) * kThreads + threadIdx.x; b < a.B_in; b += kCluster * kThreads) {
+    const int n = a.step[b];
+    const long long want = n < 0 ? 0 : clamp_tokens(a.lens_in[b], cap) + n;
+    a.lens_out[b] = static_cast<int32_t>(want < cap ? want : cap);
+  }
+  long long need = 0, total;
+  for (long long it = i_lo + threadIdx.x; it < i_hi; it += kThreads) need += a.item_need[it];
+  for (int o = 16; o; o >>= 1) need += __shfl_xor_sync(kFull, need, o);
+  block_exclusive(need, sh.scan, total);
+  if (threadIdx.x == 0) sh.totals.need = total;
+  const long long mine = count_free(a.refs_out, w_lo, w_hi);
+  const long long w_before = block_exclusive(mine, sh.scan, total);
+  if (threadIdx.x == 0) sh.totals.free_pages = total;
+  cl.sync();
+  Totals before, all;
+  exchange(cl, sh, before, all);
+  const long long take = all.need < all.free_pages ? all.need : all.free_pages;
+  if (rank == 0 && threadIdx.x == 0)
+    write_counts(a.counts, all.free_pages - take, take, all.released, all.need - take, all.bad, all.clamped, 0);
+  list_free(a.refs_out, w_lo, w_hi, before.free_pages + w_before, take, a.list, a.refs_out);
+  cl.sync();
+
+  // The items' entries, in their order.
+  long long base = before.need;
+  for (long long c0 = i_lo; c0 < i_hi; c0 += kThreads) {
+    // Rank of the first entry of each of the next kThreads items.
+    const long long it = c0 + threadIdx.x;
+    const int n = it < i_hi ? a.item_need[it] : 0;
+    long long inc = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const long long wb = block_exclusive(__shfl_sync(kFull, inc, 31), sh.scan, total);
+    const long long first = base + wb + inc - n;
+    base += total;
+    // The warp serves its own 32 items.
+    unsigned todo = __ballot_sync(kFull, n > 0);
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const long long id = c0 + warp * 32 + src;
+      long long r = __shfl_sync(kFull, first, src);
+      int32_t *out = a.table_out + (id / nseg) * mp;
+      for (int j0 = a.item_lo[id]; j0 < a.item_hi[id]; j0 += 32) {
+        const int j = j0 + lane;
+        const bool w = j < a.item_hi[id] && __ldcg(out + j) < 0;
+        const unsigned m = __ballot_sync(kFull, w);
+        if (w) {
+          const long long x = r + ballot_rank(m);
+          if (x < take) out[j] = __ldcg(a.list + x);
+        }
+        r += __popc(m);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cl.block_rank());
+  const long long P = a.num_pages, mp = a.max_pages, cap = kPage * mp < 0x7FFFFFFF ? kPage * mp : 0x7FFFFFFF;
+  const long long nseg = (mp + kSeg - 1) / kSeg;
+  const long long tid = static_cast<long long>(rank) * kThreads + threadIdx.x, threads = kCluster * kThreads;
+  if (threadIdx.x == 0) sh.totals = Totals{};
+  long long r_lo, r_hi, w_lo, w_hi, c_lo, c_hi;
+  part(P, rank, kCluster, r_lo, r_hi);
+  part(r_hi - r_lo, warp, kWarps, w_lo, w_hi);
+  w_lo += r_lo;
+  w_hi += r_lo;
+  part(a.B_out, rank, kCluster, c_lo, c_hi);  // the rows whose new pages this CTA hands out
+  for (long long b = tid; b < a.B_in; b += threads) {
+    a.children[b] = 0;
+    a.first[b] = 0x7FFFFFFF;
+  }
+  for_refs(a.refs_in, w_lo, w_hi, 0, [&](long long p, int v) {
+    if (p < w_hi) a.refs_out[p] = v;
+  });
+  cl.sync();
+
+  int bad = 0, clamped = 0, gained = 0;
+  for (long long c = tid; c < a.B_out; c += threads) {
+    const int p = a.step[c];
+    if (p >= 0 && p < a.B_in) {
+      atomicAdd(a.children + p, 1);
+      atomicMin(a.first + p, static_cast<int>(c));
+    } else if (p >= 0) {
+      ++bad;
+    }
+  }
+  cl.sync();
+
+  // Whether the last page of old row b (block col, holding page t) stays with
+  // the row's first child: nobody else may hold it.
+  auto stays = [&](int t) { return __ldcg(a.refs_in + t) == 1; };
+  // Items [0, B_in nseg): the old rows' references go, the children's come.
+  // Items from there on: the new rows.
+  const long long old_items = a.B_in * nseg, items = old_items + a.B_out * nseg;
+  for (long long it = static_cast<long long>(rank) * kWarps + warp; it < items; it += kCluster * kWarps) {
+    const bool is_new = it >= old_items;
+    const long long row = (is_new ? it - old_items : it) / nseg, seg = (is_new ? it - old_items : it) % nseg;
+    const long long j0 = seg * kSeg, j1 = j0 + kSeg < mp ? j0 + kSeg : mp;
+    const int parent = is_new ? a.step[row] : static_cast<int>(row);
+    const bool real = parent >= 0 && parent < a.B_in;
+    const int raw = real ? a.lens_in[parent] : 0;
+    const long long len = clamp_tokens(raw, cap);
+    const long long col = len % kPage ? len / kPage : -1;  // the partly filled block
+    if (!is_new && seg == 0 && lane == 0 && raw != len) ++clamped;
+    const int32_t *in = a.table_in + static_cast<long long>(real ? parent : 0) * mp;
+    const int kids = real ? __ldcg(a.children + parent) : 0;
+    if (!is_new && kids == 1 && !(col >= j0 && col < j1)) continue;  // its pages keep their references
+    const bool is_first = is_new && real && __ldcg(a.first + parent) == row;
+    int32_t *out = a.table_out + row * mp;
+    for (long long c0 = j0; c0 < j1; c0 += 32 * kUnroll) {
+      int e[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const long long j = c0 + 32 * k + lane;
+        e[k] = j < j1 && real ? in[j] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const long long j = c0 + 32 * k + lane;
+        if (j >= j1) continue;
+        const bool held = e[k] >= 0 && e[k] < P;
+        if (is_new) {
+          int v = held ? e[k] : -1;
+          bad += (!held && e[k] != -1) ? 1 : 0;
+          if (j == col) {
+            const bool copy = held && !(is_first && stays(e[k]));
+            a.item_need[row] = copy ? 1 : 0;
+            a.item_lo[row] = v;  // the page to copy from
+            if (copy) v = -1;
+          }
+          out[j] = v;
+        } else if (held) {
+          const int d = j == col ? (kids > 0 && stays(e[k]) ? 0 : -1) : kids - 1;
+          if (d) {
+            const int was = atomicAdd(a.refs_out + e[k], d);
+            gained += (was + d == 0) - (was == 0);
+          }
+        }
+      }
+    }
+    if (is_new && seg == 0 && lane == 0) {
+      a.lens_out[row] = static_cast<int32_t>(len);
+      if (col < 0) a.item_need[row] = 0;
+    }
+  }
+  add_counts(&sh.totals, 0, bad, clamped, gained);
+  const long long mine = count_free(a.refs_in, w_lo, w_hi);
+  long long total;
+  const long long w_before = block_exclusive(mine, sh.scan, total);
+  if (threadIdx.x == 0) sh.totals.free_pages = total;
+  cl.sync();
+
+  long long need = 0;
+  for (long long c = c_lo + threadIdx.x; c < c_hi; c += kThreads) need += __ldcg(a.item_need + c);
+  for (int o = 16; o; o >>= 1) need += __shfl_xor_sync(kFull, need, o);
+  block_exclusive(need, sh.scan, total);
+  if (threadIdx.x == 0) sh.totals.need = total;
+  cl.sync();
+  Totals before, all;
+  exchange(cl, sh, before, all);
+  const long long take = all.need < all.free_pages ? all.need : all.free_pages;
+  if (rank == 0 && threadIdx.x == 0)
+    write_counts(a.counts, all.free_pages + all.gained - take, take, 0, all.need - take, all.bad, all.clamped, take);
+  list_free(a.refs_in, w_lo, w_hi, before.free_pages + w_before, take, a.list, a.refs_out);
+  for (long long i = take + tid; i < a.B_out; i += threads) {
+    a.pairs[2 * i] = -1;
+    a.pairs[2 * i + 1] = -1;
+  }
+  cl.sync();
+
+  long long base = before.need;
+  for (long long c0 = c_lo; c0 < c_hi; c0 += kThreads) {
+    const long long c = c0 + threadIdx.x;
+    const bool w = c < c_hi && __ldcg(a.item_need + c) != 0;
+    const unsigned m = __ballot_sync(kFull, w);
+    const long long r = base + block_exclusive(__popc(m), sh.scan, total) + ballot_rank(m);
+    base += total;
+    if (w && r < take) {
+      const int page = __ldcg(a.list + r);
+      a.pairs[2 * r] = __ldcg(a.item_lo + c);
+      a.pairs[2 * r + 1] = page;
+      a.table_out[c * mp + clamp_tokens(a.lens_in[a.step[c]], cap) / kPage] = page;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PagesArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cl.block_rank());
+  const long long P = a.num_pages, entries = static_cast<long long>(a.B_in) * a.max_pages;
+  const long long tid = static_cast<long long>(rank) * kThreads + threadIdx.x, threads = kCluster * kThreads;
+  if (threadIdx.x == 0) sh.totals = Totals{};
+  long long r_lo, r_hi, w_lo, w_hi;
+  part(P, rank, kCluster, r_lo, r_hi);
+  part(r_hi - r_lo, warp, kWarps, w_lo, w_hi);
+  w_lo += r_lo;
+  w_hi += r_lo;
+  long long live = 0, total;
+  for_refs(a.refs_in, w_lo, w_hi, 0, [&](long long, int v) { live += __popc(__ballot_sync(kFull, v > 0)); });
+  const long long w_before = block_exclusive(live, sh.scan, total);
+  if (threadIdx.x == 0) sh.totals.need = total;
+  cl.sync();
+  Totals before, all;
+  exchange(cl, sh, before, all);
+  const long long n_live = all.need;
+
+  // Live pages below n_live stay. A hole's index is the number of holes
+  // before it; the movers are indexed from the last one down, which needs no
+  // count of those that stay.
+  long long lr = before.need + w_before;  // live pages before the next one
+  long long holes = 0;
+  for_refs(a.refs_in, w_lo, w_hi, 0, [&](long long p, int v) {
+    const bool in = p < w_hi, lv = v > 0;
+    const unsigned m = __ballot_sync(kFull, lv);
+    const long long r = lr + ballot_rank(m);
+    if (in && p < n_live) {
+      a.map[p] = lv ? static_cast<int32_t>(p) : -1;
+      if (lv) a.refs_out[p] = v;
+      else a.list[p - r] = static_cast<int32_t>(p);
+    } else if (in) {
+      if (lv) a.movers[n_live - 1 - r] = static_cast<int32_t>(p);
+      else {
+        a.map[p] = -1;
+        a.refs_out[p] = 0;
+      }
+    }
+    holes += __popc(__ballot_sync(kFull, in && p < n_live && !lv));
+    lr += __popc(m);
+  });
+  block_exclusive(holes, sh.scan, total);
+  if (threadIdx.x == 0) sh.totals.free_pages = total;
+  cl.sync();
+  exchange(cl, sh, before, all);
+  const long long moves = all.free_pages, cap = P / 2 > 1 ? P / 2 : 1;
+  for (long long i = tid; i < cap; i += threads) {
+    int src = -1, dst = -1;
+    if (i < moves) {
+      src = __ldcg(a.movers + (moves - 1 - i));
+      dst = __ldcg(a.list + i);
+      a.map[src] = dst;
+      a.refs_out[dst] = __ldcg(a.refs_in + src);
+      a.refs_out[src] = 0;
+    }
+    a.pairs[2 * i] = src;
+    a.pairs[2 * i + 1] = dst;
+  }
+  cl.sync();
+
+  int bad = 0;
+  for (long long i0 = tid; i0 < entries; i0 += threads * kUnroll) {
+    int e[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) e[k] = i0 + k * threads < entries ? a.table_in[i0 + k * threads] : -1;
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const bool held = e[k] >= 0 && e[k] < P;
+      bad += (!held && e[k] != -1) ? 1 : 0;
+      e[k] = held ? __ldcg(a.map + e[k]) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (i0 + k * threads < entries) a.table_out[i0 + k * threads] = e[k];
+  }
+  add_counts(&sh.totals, 0, bad, 0, 0);
+  cl.sync();
+  if (rank == 0) {
+    exchange(cl, sh, before, all);
+    if (threadIdx.x == 0) write_counts(a.counts, P - n_live, 0, 0, 0, all.bad, 0, moves);
+  }
+  cl.sync();  // the others' counts have been read before they leave
+}
+
+// Pages src -> dst of both pools in every layer. A warp copies pieces of
+// kPiece bytes, four 16-byte loads in flight per lane before the first store.
+constexpr int kPiece = 32 * 16 * 4;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyBlocksPerSm = 8;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
+  long long n = a.max_pairs;
+  if (a.counts) {
+    const long long c = a.counts[6];
+    n = c < 0 ? 0 : (c < n ? c : n);
+  }
+  const int lane = threadIdx.x & 31;
+  const unsigned kp = static_cast<unsigned>((a.k_bytes + kPiece - 1) / kPiece);
+  const unsigned pieces = kp + static_cast<unsigned>((a.v_bytes + kPiece - 1) / kPiece);  // of one page in one layer
+  const long long units = n * a.n_layers * pieces;
+  const long long warps = static_cast<long long>(gridDim.x) * (kCopyThreads / 32);
+  unsigned bad = 0;
+  for (long long u = (static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5; u < units; u += warps) {
+    const long long pl = u / pieces;
+    const unsigned piece = static_cast<unsigned>(u - pl * pieces);
+    const long long layer = pl / n, i = pl - layer * n;
+    const int src = a.pairs[2 * i], dst = a.pairs[2 * i + 1];
+    if (src < 0 && dst < 0) continue;
+    if (src < 0 || dst < 0 || src >= a.num_pages || dst >= a.num_pages) {
+      if (layer == 0 && piece == 0) ++bad;
+      continue;
+    }
+    const bool is_k = piece < kp;
+    const int64_t bytes = is_k ? a.k_bytes : a.v_bytes;
+    uint8_t *pool = is_k ? a.kpool + layer * a.k_stride : a.vpool + layer * a.v_stride;
+    const int64_t at = static_cast<int64_t>(is_k ? piece : piece - kp) * kPiece + lane * 16;
+    const uint8_t *from = pool + src * bytes + at;
+    uint8_t *to = pool + dst * bytes + at;
+    uint4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + 512 * k < bytes) x[k] = __ldcs(reinterpret_cast<const uint4 *>(from + 512 * k));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + 512 * k < bytes) __stcs(reinterpret_cast<uint4 *>(to + 512 * k), x[k]);
+  }
+  if (a.stats && lane == 0 && bad) atomicAdd(&a.stats->bad_pages, static_cast<unsigned long long>(bad));
+}
+
+template <auto Kern>
+int launch_cluster(const PagesArgs &a, cudaStream_t st) {
+  const cudaError_t e = allow_wide_cluster<Kern>();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kCluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, Kern, a));
+}
+
+}  // namespace
+
+PagesLayout pages_layout(int64_t num_pages, int64_t B, int64_t max_pages) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  PagesLayout l;
+  const size_t rows = static_cast<size_t>(B), pages = static_cast<size_t>(num_pages);
+  const size_t items = rows * ((max_pages + kSeg - 1) / kSeg);
+  l.list = 0;  // the pages handed out, or a hole per move: never more than there are pages
+  l.need = l.list + up(4 * pages);
+  l.lo = l.need + up(4 * items);
+  l.hi = l.lo + up(4 * items);
+  l.map = l.hi + up(4 * items);                               // compact: new numbers; fork: children of each row
+  l.movers = l.map + up(4 * std::max(pages, rows));           // compact: pages that move; fork: first children
+  l.total = l.movers + up(4 * std::max(pages / 2 + 1, rows));
+  return l;
+}
+
+int launch_pages_advance(const PagesArgs &a, void *stream) {
+  return launch_cluster<advance_kernel>(a, static_cast<cudaStream_t>(stream));
+}
+int launch_pages_fork(const PagesArgs &a, void *stream) {
+  return launch_cluster<fork_kernel>(a, static_cast<cudaStream_t>(stream));
+}
+int launch_pages_compact(const PagesArgs &a, void *stream) {
+  return launch_cluster<compact_kernel>(a, static_cast<cudaStream_t>(stream));
+}
+
+int launch_pages_copy(const CopyArgs &a, int sm_count, void *stream) {
+  const int64_t pieces = (a.k_bytes + kPiece - 1) / kPiece + (a.v_bytes + kPiece - 1) / kPiece;
+  const int64_t most = a.max_pairs * a.n_layers * pieces;  // warps that could have work
+  const int64_t blocks = (most + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+  const int64_t full = static_cast<int64_t>(sm_count) * kCopyBlocksPerSm;
+  copy_kernel<<<static_cast<unsigned>(blocks < full ? blocks : full), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace dqi

@@ -423,6 +423,103 @@ int dq_prefill_attention_window_paged(const dq_tables *t, const void *q, int q_d
                                       int out_dtype, void *d_workspace, size_t ws_bytes,
                                       dq_stats *d_stats, void *stream);
 
+/* The pages of a paged cache. The state of a cache is three device arrays of
+ * int32: refs [num_pages], the references that each page has (0: free; the
+ * caller may hold references of its own, for a stored prefix for instance);
+ * the page table [B][max_pages] (-1: no page); and the lengths [B]. Each
+ * call reads one state and writes the next one, so that a caller who runs out
+ * of pages still has the old one to try again with; nothing is read back to
+ * the host and a call can be captured in a graph. The results are whole
+ * numbers determined by the state alone. One table and one refs array serve
+ * all layers: page p of every layer's pool belongs to the same tokens.
+ *   num_pages   1 .. 2^31 - 1
+ *   max_pages   pages per row, 1 .. 2^26 (a row's tokens are counted in int32)
+ *   d_counts    device dq_page_counts, written by every call
+ *   d_workspace device, 16-byte aligned, dq_pages_workspace_bytes(t, num_pages,
+ *               the most rows of the two tables, max_pages); contents need not
+ *               be initialised; calls sharing it must not overlap on the GPU
+ * A table entry outside [0, num_pages) other than -1 counts in `bad` and is
+ * -1 in the new table; a length outside [0, 32 max_pages] is clamped and
+ * counted. Arrays of no rows may be NULL. Errors: DQ_ERR_NULL, _SHAPE, _ALIGN
+ * (4 bytes; workspace 16), _WORKSPACE, _DEVICE, _CUDA. */
+typedef struct {
+  int32_t free_pages; /* pages without a reference after the call            */
+  int32_t taken;      /* pages handed out                                    */
+  int32_t released;   /* references that dq_pages_advance gave back          */
+  int32_t short_of;   /* pages that were wanted and not there (entry -1)     */
+  int32_t bad;        /* table entries or parents out of range               */
+  int32_t clamped;    /* lengths out of range                                */
+  int32_t pairs;      /* page copies listed (dq_pages_fork, _compact)        */
+  int32_t reserved;   /* 0                                                   */
+} dq_page_counts;
+
+size_t dq_pages_workspace_bytes(const dq_tables *t, int64_t num_pages, int B,
+                                int64_t max_pages);
+
+/* Makes room for the next tokens of every sequence and gives back what none
+ * of them sees. With L = d_lens[b] and n = d_n_new[b]:
+ *   n < 0    the sequence ends: all its references go, its new length is 0
+ *   n >= 0   its new length is L + n (at most 32 max_pages, else clamped).
+ *            With window > 0 the pages that lie wholly in [sinks, L + 1 -
+ *            window) go: no query from position L on sees them (see
+ *            dq_decode_attention_window). Then every entry without a page
+ *            among those of tokens L .. L + n - 1 gets one.
+ * Pages are handed out after all releases, lowest free page first, in the
+ * order of the rows and of their entries. window 0 keeps everything. Each
+ * output may be the input itself. */
+int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
+                     const int32_t *d_page_table, int64_t max_pages,
+                     const int32_t *d_lens, const int32_t *d_n_new, int B,
+                     int64_t window, int64_t sinks, int32_t *d_refs_out,
+                     int32_t *d_page_table_out, int32_t *d_lens_out,
+                     dq_page_counts *d_counts, void *d_workspace, size_t ws_bytes,
+                     void *stream);
+
+/* Forks sequences: row c of the new table is old row d_parent[c], with its
+ * length; a negative parent gives an empty row (one of B_in or more too, and
+ * counts in `bad`). Old rows that are nobody's parent are thereby dropped.
+ * Pages are shared, except for a row's last page where it is partly filled
+ * (the children will write to it): the parent's first child keeps it, if the
+ * parent's row had its only reference; every other child gets the lowest free
+ * page of the old state, and d_pairs [B_out][2] the copy to make (source,
+ * destination; then -1, -1). Where pages run short the entry is -1. Outputs
+ * must not be inputs (DQ_ERR_SHAPE). dq_pages_copy makes the copies, before
+ * the next append. */
+int dq_pages_fork(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
+                  const int32_t *d_page_table, int64_t max_pages,
+                  const int32_t *d_lens, int B_in, const int32_t *d_parent,
+                  int B_out, int32_t *d_refs_out, int32_t *d_page_table_out,
+                  int32_t *d_lens_out, int32_t *d_pairs, dq_page_counts *d_counts,
+                  void *d_workspace, size_t ws_bytes, void *stream);
+
+/* Moves the n = num_pages - free_pages pages with a reference to the numbers
+ * 0 .. n - 1: those below n stay, the others fill the holes, both in ascending
+ * order. d_pairs [max(1, num_pages / 2)][2] lists the moves (then -1, -1);
+ * refs and table are renumbered (an entry whose page has no reference becomes
+ * -1). References that the caller holds outside the table are the caller's to
+ * renumber. Each output may be the input itself. dq_pages_copy makes the
+ * moves; sources and destinations are disjoint. */
+int dq_pages_compact(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
+                     const int32_t *d_page_table, int64_t max_pages, int B,
+                     int32_t *d_refs_out, int32_t *d_page_table_out,
+                     int32_t *d_pairs, dq_page_counts *d_counts, void *d_workspace,
+                     size_t ws_bytes, void *stream);
+
+/* Copies pages in the K and V pools of n_layers layers: pair i's source to its
+ * destination, for the first d_counts->pairs pairs (d_counts NULL: for all
+ * max_pairs; at most max_pairs either way). A pair of two negative numbers is
+ * skipped; any other outside [0, num_pages) too, and counts in
+ * d_stats->bad_pages. A page that is a destination twice, or a source and a
+ * destination, holds one of the copies' bytes or a mixture.
+ *   d_kpool, d_vpool  the first layer's pools, 16-byte aligned
+ *   *_layer_stride    bytes from one layer's pool to the next, a multiple of
+ *                     16 (else DQ_ERR_ALIGN) */
+int dq_pages_copy(const dq_tables *t, uint8_t *d_kpool, uint8_t *d_vpool,
+                  int64_t num_pages, int64_t n_layers, int64_t k_layer_stride,
+                  int64_t v_layer_stride, const int32_t *d_pairs,
+                  int64_t max_pairs, const dq_page_counts *d_counts,
+                  dq_stats *d_stats, void *stream);
+
 /* Test hook: decodes n flat containers of one stream.
  *   d_cache   device [n][C]; d_syms device uint8 [n][128]; d_norm16 device
  *             uint16 [n]; d_status device int32 [n] (may be NULL)
