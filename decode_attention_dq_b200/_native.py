@@ -136,6 +136,10 @@ def _ptr(t):
     return C.c_void_p(t.data_ptr()) if t is not None else None
 
 
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -372,46 +376,59 @@ def dq_prefill_attention_paged(tab: Tables, q: torch.Tensor, kpool: torch.Tensor
         _ptr(stats), _stream(stream)))
 
 
-def _check_cuda(**tensors) -> None:
-    """Each tensor on one CUDA device and contiguous (the calls take plain pointers)."""
-    device = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
+def _check_cuda(names: str, *tensors) -> None:
+    """Each tensor contiguous and on the current CUDA device (the calls take
+    plain pointers). `names`: what the messages call them, in order."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != device or device < 0 or not t.is_contiguous():
+            break
+    else:
+        if device == torch.cuda.current_device():
+            return
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+    for name, t in zip(names.split(), tensors):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("%s must be a contiguous CUDA tensor" % name)
-        if device is not None and t.device != device:
-            raise ValueError("%s is on %s, the others on %s" % (name, t.device, device))
-        device = t.device
+        if t.get_device() != device:
+            raise ValueError("%s is on %s, the others on cuda:%d" % (name, t.device, device))
 
 
-def _check_heads(tab, q, out, kcache, vcache):
+def _check_int32(names: str, *pairs) -> None:
+    """Each (tensor, shape): an int32 tensor of that shape."""
+    for k, (t, shape) in enumerate(pairs):
+        if t.dtype is not torch.int32 or t.shape != shape:
+            raise ValueError("%s must be int32 %s, got %s %s" % (names.split()[k], shape, t.dtype, tuple(t.shape)))
+
+
+def _check_stats(stats) -> None:
+    if stats is not None:
+        _check_cuda("stats", stats)
+
+
+def _check_heads(q, out, kcache, vcache) -> None:
     if q.shape[-1] != 128 or out.shape != q.shape:
-        raise ValueError("q and out must have one shape with 128 coordinates, got %s and %s" % (q.shape, out.shape))
-    if kcache.dtype != torch.uint8 or vcache.dtype != torch.uint8 or kcache.dim() != 4 or vcache.dim() != 4:
-        raise ValueError("caches must be 4-dimensional uint8 tensors")
-    if kcache.shape[:2] != vcache.shape[:2]:
-        raise ValueError("K and V caches differ in shape: %s and %s" % (kcache.shape, vcache.shape))
+        raise ValueError("q and out must have one shape with 128 coordinates, got %s and %s" % (tuple(q.shape), tuple(out.shape)))
+    if kcache.dtype is not torch.uint8 or vcache.dtype is not torch.uint8:
+        raise ValueError("caches must be uint8, got %s and %s" % (kcache.dtype, vcache.dtype))
 
 
-def _check_contiguous_cache(tab, B, kcache, vcache):
-    T_cap = kcache.shape[2]
-    want = tuple((B, tab.n_kv_heads, T_cap, s.container_bytes) for s in (tab.k, tab.v))
-    if (tuple(kcache.shape), tuple(vcache.shape)) != want:
-        raise ValueError("caches must be %s and %s, got %s and %s" % (*want, tuple(kcache.shape), tuple(vcache.shape)))
+def _check_shapes(what: str, k, v, k_shape, v_shape) -> None:
+    if k.shape != k_shape or v.shape != v_shape:
+        raise ValueError("%s must be %s and %s, got %s and %s" % (what, k_shape, v_shape, tuple(k.shape), tuple(v.shape)))
 
 
-def _check_pools(tab, B, kpool, vpool, page_table):
-    want = tuple((kpool.shape[0], tab.n_kv_heads, s.container_bytes, 32) for s in (tab.k, tab.v))
-    if (tuple(kpool.shape), tuple(vpool.shape)) != want:
-        raise ValueError("pools must be %s and %s, got %s and %s" % (*want, tuple(kpool.shape), tuple(vpool.shape)))
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be int32 [%d, max_pages]" % B)
+def _check_contiguous_cache(tab, B, kcache, vcache) -> None:
+    T_cap = kcache.shape[-2]
+    _check_shapes("caches", kcache, vcache, (B, tab.n_kv_heads, T_cap, tab.k.container_bytes),
+                  (B, tab.n_kv_heads, T_cap, tab.v.container_bytes))
 
 
-def _check_lens(name, t, B):
-    if t.dtype != torch.int32 or tuple(t.shape) != (B,):
-        raise ValueError("%s must be int32 [%d], got %s %s" % (name, B, t.dtype, tuple(t.shape)))
+def _check_pools(tab, B, kpool, vpool, page_table) -> None:
+    P = kpool.shape[0]
+    _check_shapes("pools", kpool, vpool, (P, tab.n_kv_heads, tab.k.container_bytes, 32),
+                  (P, tab.n_kv_heads, tab.v.container_bytes, 32))
+    _check_int32("page_table", (page_table, (B, page_table.shape[-1])))
 
 
 def dq_decode_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
@@ -420,15 +437,18 @@ def dq_decode_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tenso
                                stats: torch.Tensor | None = None, stream=None) -> None:
     """dq_decode_attention over the last `window` tokens and the first `sinks`
     ones of each sequence; what lies between is never read."""
-    _check_cuda(q=q, kcache=kcache, vcache=vcache, seq_lens=seq_lens, out=out, workspace=workspace, stats=stats)
-    _check_heads(tab, q, out, kcache, vcache)
+    _check_cuda("q kcache vcache seq_lens out workspace", q, kcache, vcache, seq_lens, out, workspace)
+    _check_stats(stats)
+    _check_heads(q, out, kcache, vcache)
     B, Hq, _ = q.shape
     _check_contiguous_cache(tab, B, kcache, vcache)
-    _check_lens("seq_lens", seq_lens, B)
+    _check_int32("seq_lens", (seq_lens, (B,)))
+    if q.numel() == 0:
+        return
     _check("dq_decode_attention_window", load().dq_decode_attention_window(
-        tab.handle, _ptr(q), _dtype_code(q), _ptr(kcache), _ptr(vcache), _ptr(seq_lens), B, Hq, kcache.shape[1],
-        kcache.shape[2], T_max, window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out),
-        _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(stats),
+        tab.handle, q.data_ptr(), _dtype_code(q), kcache.data_ptr(), vcache.data_ptr(), seq_lens.data_ptr(), B, Hq, kcache.shape[1],
+        kcache.shape[2], T_max, window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), out.data_ptr(),
+        _dtype_code(out), workspace.data_ptr(), workspace.nbytes, _addr(stats),
         _stream(stream)))
 
 
@@ -439,17 +459,19 @@ def dq_decode_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch.
                                      stream=None) -> None:
     """dq_decode_attention_window over page pools; page-table entries between
     the first tokens and the window may be -1."""
-    _check_cuda(q=q, kpool=kpool, vpool=vpool, page_table=page_table, seq_lens=seq_lens, out=out,
-                workspace=workspace, stats=stats)
-    _check_heads(tab, q, out, kpool, vpool)
+    _check_cuda("q kpool vpool page_table seq_lens out workspace", q, kpool, vpool, page_table, seq_lens, out, workspace)
+    _check_stats(stats)
+    _check_heads(q, out, kpool, vpool)
     B, Hq, _ = q.shape
     _check_pools(tab, B, kpool, vpool, page_table)
-    _check_lens("seq_lens", seq_lens, B)
+    _check_int32("seq_lens", (seq_lens, (B,)))
+    if q.numel() == 0:
+        return
     _check("dq_decode_attention_window_paged", load().dq_decode_attention_window_paged(
-        tab.handle, _ptr(q), _dtype_code(q), _ptr(kpool), _ptr(vpool), kpool.shape[0], _ptr(page_table),
-        page_table.shape[1], _ptr(seq_lens), B, Hq, kpool.shape[1], T_max, window, sinks,
-        float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(stats), _stream(stream)))
+        tab.handle, q.data_ptr(), _dtype_code(q), kpool.data_ptr(), vpool.data_ptr(), kpool.shape[0], page_table.data_ptr(),
+        page_table.shape[1], seq_lens.data_ptr(), B, Hq, kpool.shape[1], T_max, window, sinks,
+        float(128 ** -0.5 if sm_scale is None else sm_scale), out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
+        workspace.nbytes, _addr(stats), _stream(stream)))
 
 
 def dq_prefill_window_workspace_bytes(tab: Tables, B: int, Hkv: int, T_cap: int, n_q: int, window: int,
@@ -465,18 +487,22 @@ def dq_prefill_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tens
     """dq_prefill_attention whose query at position p sees the tokens p -
     window + 1 .. p and the first `sinks` ones; workspace uint8 of
     dq_prefill_window_workspace_bytes (allocated if None)."""
-    _check_cuda(q=q, kcache=kcache, vcache=vcache, q_start=q_start, out=out, workspace=workspace, stats=stats)
-    _check_heads(tab, q, out, kcache, vcache)
+    _check_cuda("q kcache vcache q_start out", q, kcache, vcache, q_start, out)
+    _check_stats(stats)
+    _check_heads(q, out, kcache, vcache)
     B, n_q, Hq, _ = q.shape
     _check_contiguous_cache(tab, B, kcache, vcache)
-    _check_lens("q_start", q_start, B)
+    _check_int32("q_start", (q_start, (B,)))
+    if q.numel() == 0:
+        return
     if workspace is None:
         workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kcache.shape[1], kcache.shape[2], n_q,
                                                                   window, sinks), dtype=torch.uint8, device=q.device)
+    _check_cuda("q workspace", q, workspace)
     _check("dq_prefill_attention_window", load().dq_prefill_attention_window(
-        tab.handle, _ptr(q), _dtype_code(q), _ptr(kcache), _ptr(vcache), _ptr(q_start), B, n_q, Hq, kcache.shape[1],
-        kcache.shape[2], window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out),
-        _dtype_code(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(stats),
+        tab.handle, q.data_ptr(), _dtype_code(q), kcache.data_ptr(), vcache.data_ptr(), q_start.data_ptr(), B, n_q, Hq, kcache.shape[1],
+        kcache.shape[2], window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), out.data_ptr(),
+        _dtype_code(out), workspace.data_ptr(), workspace.nbytes, _addr(stats),
         _stream(stream)))
 
 
@@ -487,21 +513,24 @@ def dq_prefill_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch
                                       stream=None) -> None:
     """dq_prefill_attention_window over page pools; page-table entries that no
     query of the chunk sees may be -1."""
-    _check_cuda(q=q, kpool=kpool, vpool=vpool, page_table=page_table, q_start=q_start, out=out,
-                workspace=workspace, stats=stats)
-    _check_heads(tab, q, out, kpool, vpool)
+    _check_cuda("q kpool vpool page_table q_start out", q, kpool, vpool, page_table, q_start, out)
+    _check_stats(stats)
+    _check_heads(q, out, kpool, vpool)
     B, n_q, Hq, _ = q.shape
     _check_pools(tab, B, kpool, vpool, page_table)
-    _check_lens("q_start", q_start, B)
+    _check_int32("q_start", (q_start, (B,)))
+    if q.numel() == 0:
+        return
     if workspace is None:
         workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kpool.shape[1], 32 * page_table.shape[1],
                                                                   n_q, window, sinks),
                                 dtype=torch.uint8, device=q.device)
+    _check_cuda("q workspace", q, workspace)
     _check("dq_prefill_attention_window_paged", load().dq_prefill_attention_window_paged(
-        tab.handle, _ptr(q), _dtype_code(q), _ptr(kpool), _ptr(vpool), kpool.shape[0], _ptr(page_table),
-        page_table.shape[1], _ptr(q_start), B, n_q, Hq, kpool.shape[1], window, sinks,
-        float(128 ** -0.5 if sm_scale is None else sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(stats), _stream(stream)))
+        tab.handle, q.data_ptr(), _dtype_code(q), kpool.data_ptr(), vpool.data_ptr(), kpool.shape[0], page_table.data_ptr(),
+        page_table.shape[1], q_start.data_ptr(), B, n_q, Hq, kpool.shape[1], window, sinks,
+        float(128 ** -0.5 if sm_scale is None else sm_scale), out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
+        workspace.nbytes, _addr(stats), _stream(stream)))
 
 
 def new_page_state(num_pages: int, B: int, max_pages: int, device=None):
@@ -521,13 +550,6 @@ def page_counts_dict(counts: torch.Tensor) -> dict:
     return dict(zip(PAGE_COUNT_FIELDS, counts.cpu().tolist()))
 
 
-def _check_int32(**tensors) -> None:
-    """Name = (tensor, shape): an int32 tensor of that shape."""
-    for name, (t, shape) in tensors.items():
-        if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-            raise ValueError("%s must be int32 %s, got %s %s" % (name, tuple(shape), t.dtype, tuple(t.shape)))
-
-
 def dq_pages_workspace_bytes(tab: Tables, num_pages: int, B: int, max_pages: int) -> int:
     """Bytes of the workspace of dq_pages_advance, _fork and _compact for tables of at most B rows."""
     return int(load().dq_pages_workspace_bytes(tab.handle, num_pages, B, max_pages))
@@ -541,17 +563,16 @@ def dq_pages_advance(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, 
     the sequence ends); with a window the pages behind it go back. int32: refs
     [num_pages], page_table [B, max_pages], lens and n_new [B]; the outputs may
     be the inputs."""
-    _check_cuda(refs=refs, page_table=page_table, lens=lens, n_new=n_new, refs_out=refs_out,
-                page_table_out=page_table_out, lens_out=lens_out, counts=counts, workspace=workspace)
-    B, max_pages = page_table.shape
+    _check_cuda("refs page_table lens n_new refs_out page_table_out lens_out counts workspace", refs, page_table, lens,
+                n_new, refs_out, page_table_out, lens_out, counts, workspace)
+    B, max_pages = rows = page_table.shape
     P = refs.numel()
-    _check_int32(refs=(refs, (P,)), page_table=(page_table, (B, max_pages)), lens=(lens, (B,)), n_new=(n_new, (B,)),
-                 refs_out=(refs_out, (P,)), page_table_out=(page_table_out, (B, max_pages)),
-                 lens_out=(lens_out, (B,)), counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check_int32("refs page_table lens n_new refs_out page_table_out lens_out counts", (refs, (P,)), (page_table, rows),
+                 (lens, (B,)), (n_new, (B,)), (refs_out, (P,)), (page_table_out, rows), (lens_out, (B,)), (counts, (8,)))
     _check("dq_pages_advance", load().dq_pages_advance(
-        tab.handle, P, _ptr(refs), _ptr(page_table), max_pages, _ptr(lens), _ptr(n_new), B, window, sinks,
-        _ptr(refs_out), _ptr(page_table_out), _ptr(lens_out), _ptr(counts), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        tab.handle, P, refs.data_ptr(), page_table.data_ptr(), max_pages, lens.data_ptr(), n_new.data_ptr(), B, window, sinks,
+        refs_out.data_ptr(), page_table_out.data_ptr(), lens_out.data_ptr(), counts.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _stream(stream)))
 
 
 def dq_pages_fork(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
@@ -562,18 +583,17 @@ def dq_pages_fork(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, len
     one (negative: empty). Pages are shared; pairs [B_out, 2] lists the copies
     of partly filled last pages for dq_pages_copy. Outputs must be other
     tensors than the inputs."""
-    _check_cuda(refs=refs, page_table=page_table, lens=lens, parent=parent, refs_out=refs_out,
-                page_table_out=page_table_out, lens_out=lens_out, pairs=pairs, counts=counts, workspace=workspace)
-    B, max_pages = page_table.shape
+    _check_cuda("refs page_table lens parent refs_out page_table_out lens_out pairs counts workspace", refs, page_table,
+                lens, parent, refs_out, page_table_out, lens_out, pairs, counts, workspace)
+    B, max_pages = rows = page_table.shape
     P, B_out = refs.numel(), parent.numel()
-    _check_int32(refs=(refs, (P,)), page_table=(page_table, (B, max_pages)), lens=(lens, (B,)),
-                 parent=(parent, (B_out,)), refs_out=(refs_out, (P,)),
-                 page_table_out=(page_table_out, (B_out, max_pages)), lens_out=(lens_out, (B_out,)),
-                 pairs=(pairs, (B_out, 2)), counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check_int32("refs page_table lens parent refs_out page_table_out lens_out pairs counts", (refs, (P,)),
+                 (page_table, rows), (lens, (B,)), (parent, (B_out,)), (refs_out, (P,)),
+                 (page_table_out, (B_out, max_pages)), (lens_out, (B_out,)), (pairs, (B_out, 2)), (counts, (8,)))
     _check("dq_pages_fork", load().dq_pages_fork(
-        tab.handle, P, _ptr(refs), _ptr(page_table), max_pages, _ptr(lens), B, _ptr(parent), B_out, _ptr(refs_out),
-        _ptr(page_table_out), _ptr(lens_out), _ptr(pairs), _ptr(counts), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        tab.handle, P, refs.data_ptr(), page_table.data_ptr(), max_pages, lens.data_ptr(), B, parent.data_ptr(), B_out, refs_out.data_ptr(),
+        page_table_out.data_ptr(), lens_out.data_ptr(), pairs.data_ptr(), counts.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _stream(stream)))
 
 
 def dq_pages_compact(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, refs_out: torch.Tensor,
@@ -582,16 +602,15 @@ def dq_pages_compact(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, 
     """Renumbers the pages in use to the lowest numbers; pairs [max(1,
     num_pages // 2), 2] lists the moves for dq_pages_copy. The outputs may be
     the inputs."""
-    _check_cuda(refs=refs, page_table=page_table, refs_out=refs_out, page_table_out=page_table_out, pairs=pairs,
-                counts=counts, workspace=workspace)
-    B, max_pages = page_table.shape
+    _check_cuda("refs page_table refs_out page_table_out pairs counts workspace", refs, page_table, refs_out,
+                page_table_out, pairs, counts, workspace)
+    B, max_pages = rows = page_table.shape
     P = refs.numel()
-    _check_int32(refs=(refs, (P,)), page_table=(page_table, (B, max_pages)), refs_out=(refs_out, (P,)),
-                 page_table_out=(page_table_out, (B, max_pages)), pairs=(pairs, (max(1, P // 2), 2)),
-                 counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+    _check_int32("refs page_table refs_out page_table_out pairs counts", (refs, (P,)), (page_table, rows),
+                 (refs_out, (P,)), (page_table_out, rows), (pairs, (max(1, P // 2), 2)), (counts, (8,)))
     _check("dq_pages_compact", load().dq_pages_compact(
-        tab.handle, P, _ptr(refs), _ptr(page_table), max_pages, B, _ptr(refs_out), _ptr(page_table_out), _ptr(pairs),
-        _ptr(counts), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        tab.handle, P, refs.data_ptr(), page_table.data_ptr(), max_pages, B, refs_out.data_ptr(), page_table_out.data_ptr(), pairs.data_ptr(),
+        counts.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream)))
 
 
 def dq_pages_copy(tab: Tables, kpool: torch.Tensor, vpool: torch.Tensor, pairs: torch.Tensor,
@@ -599,24 +618,24 @@ def dq_pages_copy(tab: Tables, kpool: torch.Tensor, vpool: torch.Tensor, pairs: 
     """Copies the pages that pairs int32 [n, 2] names (source, destination) in
     pools [num_pages, Hkv, C, 32], or [layers, num_pages, Hkv, C, 32] (each
     layer contiguous): the first counts.pairs of them, or all."""
-    _check_cuda(pairs=pairs, counts=counts, stats=stats)
-    kl, vl = (p if p.dim() == 5 else p.unsqueeze(0) for p in (kpool, vpool))
-    if kl.dim() != 5 or vl.dim() != 5 or kl.shape[0] != vl.shape[0]:
-        raise ValueError("pools must have 4 dimensions, or 5 with as many layers, got %s and %s"
-                         % (tuple(kpool.shape), tuple(vpool.shape)))
-    if kl.shape[0] == 0:
+    if kpool.dim() == 4:
+        kpool, vpool = kpool.unsqueeze(0), vpool.unsqueeze(0)
+    L, P = kpool.shape[:2]
+    _check_shapes("pools", kpool, vpool, (L, P, tab.n_kv_heads, tab.k.container_bytes, 32),
+                  (L, P, tab.n_kv_heads, tab.v.container_bytes, 32))
+    if kpool.dtype is not torch.uint8 or vpool.dtype is not torch.uint8:
+        raise ValueError("pools must be uint8, got %s and %s" % (kpool.dtype, vpool.dtype))
+    if L == 0:
         return
-    _check_cuda(kpool=kl[0], vpool=vl[0], pairs=pairs)
-    for name, p, s in (("kpool", kl, tab.k), ("vpool", vl, tab.v)):
-        want = (kl.shape[1], tab.n_kv_heads, s.container_bytes, 32)
-        if p.dtype != torch.uint8 or tuple(p.shape[1:]) != want:
-            raise ValueError("%s must be uint8 %s in each layer, got %s %s" % (name, want, p.dtype, tuple(p.shape)))
-    _check_int32(pairs=(pairs, (pairs.shape[0], 2)))
+    _check_cuda("kpool vpool pairs", kpool[0], vpool[0], pairs)
+    _check_int32("pairs", (pairs, (pairs.shape[0], 2)))
     if counts is not None:
-        _check_int32(counts=(counts, (len(PAGE_COUNT_FIELDS),)))
+        _check_cuda("counts pairs", counts, pairs)
+        _check_int32("counts", (counts, (8,)))
+    _check_stats(stats)
     _check("dq_pages_copy", load().dq_pages_copy(
-        tab.handle, _ptr(kl), _ptr(vl), kl.shape[1], kl.shape[0], kl.stride(0), vl.stride(0), _ptr(pairs),
-        pairs.shape[0], _ptr(counts), _ptr(stats), _stream(stream)))
+        tab.handle, kpool.data_ptr(), vpool.data_ptr(), P, L, kpool.stride(0), vpool.stride(0), pairs.data_ptr(),
+        pairs.shape[0], _addr(counts), _addr(stats), _stream(stream)))
 
 
 def dq_decode_symbols(tab: Tables, cache: torch.Tensor, kind: int, syms: torch.Tensor,

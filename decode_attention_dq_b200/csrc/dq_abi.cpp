@@ -71,14 +71,15 @@ double f16_to_double(uint16_t h) {
 
 // Scale kappa in [1, 2) (steps of 2^-16) that minimises the largest relative
 // error of fp16(kappa * level) over the non-zero levels; the smallest such
-// kappa on ties.
+// kappa on ties. (The error only grows with each level: a candidate is
+// dropped once it is no better than the best so far.)
 void choose_tile_scale(const dqi::StreamDesign &d, dqi::DevStream *s) {
   double best_err = INFINITY;
   double best_k = 1.0;
   for (int j = 0; j < 65536; ++j) {
     const double kappa = 1.0 + j / 65536.0;
     double err = 0.0;
-    for (int i = 0; i < d.n_levels; ++i) {
+    for (int i = 0; i < d.n_levels && err < best_err; ++i) {
       const double y = static_cast<double>(d.levels[i]);
       if (y == 0.0) continue;
       const double h = f16_to_double(f32_to_f16_rn(static_cast<float>(kappa * y)));
@@ -91,8 +92,14 @@ void choose_tile_scale(const dqi::StreamDesign &d, dqi::DevStream *s) {
   }
   s->tile_scale = static_cast<float>(best_k);
   s->tile_rel_err = static_cast<float>(best_err);
-  for (int i = 0; i < dqi::kMaxLevels; ++i)
-    s->level16[i] = i < d.n_levels ? f32_to_f16_rn(static_cast<float>(best_k * static_cast<double>(d.levels[i]))) : 0u;
+  for (int i = 0; i < dqi::kMaxLevels; ++i) {
+    s->level16[i] = 0u;
+    if (i >= d.n_levels) continue;
+    const double y = best_k * static_cast<double>(d.levels[i]);
+    const uint16_t hi = f32_to_f16_rn(static_cast<float>(y));
+    const uint16_t lo = f32_to_f16_rn(static_cast<float>(y - f16_to_double(hi)));
+    s->level16[i] = static_cast<uint32_t>(hi) | static_cast<uint32_t>(lo) << 16;
+  }
 }
 
 // Scale kappa in [1, 2) (steps of 2^-16) for the prefill score operand:
@@ -105,7 +112,7 @@ void choose_score_scale(const dqi::StreamDesign &d, dqi::DevStream *s) {
   for (int j = 0; j < 65536; ++j) {
     const double kappa = 1.0 + j / 65536.0;
     double err = 0.0;
-    for (int i = 0; i < d.n_levels; ++i) {
+    for (int i = 0; i < d.n_levels && err < best_err; ++i) {
       const double y = static_cast<double>(d.levels[i]);
       const double h = f16_to_double(f32_to_f16_rn(static_cast<float>(kappa * y)));
       err += static_cast<double>(d.freq[i]) * std::fabs(h / kappa - y);

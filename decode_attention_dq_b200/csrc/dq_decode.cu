@@ -41,6 +41,11 @@
 // (hundreds of slots per row) and 4 otherwise:
 //   D7  log-sum-exp merge of the slots of (b, h), o = D H o_rot / (128 l)
 //
+// With fp32 outputs of a windowed call (kLo) V's levels go through the tile as
+// two fp16 values each, 32 coordinates at a time: kappa y is then exact to
+// 2^-22, as the weights are, and the output keeps fp32's accuracy. bf16
+// outputs round by 2^-9, far above the few 1e-5 of a single fp16 level.
+//
 // With a sliding window (kWin) the flat order holds the visible groups only:
 // of each sequence the groups of the first tokens, then those from the
 // window's first token on. Nothing else changes: the hidden groups take no
@@ -238,6 +243,39 @@ __device__ __forceinline__ void pv_mma_half(float (&c)[kD / 16][4], uint32_t til
   }
 }
 
+// The same for 32 coordinates whose levels lie as fp16 values in the tile's
+// first four chunks and as fp16 remainders in the other four (the product of
+// the weights' and the levels' low parts, 2^-22 of the result, is left out).
+template <int quarter>
+__device__ __forceinline__ void pv_mma_quarter(float (&c)[kD / 16][4], uint32_t tile_s, const uint32_t (&bh)[2][2],
+                                               const uint32_t (&bl)[2][2], int lane) {
+  const int r = (lane & 7) + ((lane >> 4) & 1) * 8;
+  const int cadd = (lane >> 3) & 1;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t a[4], z[4];
+      ldsm_x4_trans(a, tile_s + tile_off(ks * 16 + r, 2 * mt + cadd));
+      ldsm_x4_trans(z, tile_s + tile_off(ks * 16 + r, 4 + 2 * mt + cadd));
+      mma_16816(c[quarter * 2 + mt], a, bh[ks][0], bh[ks][1]);
+      mma_16816(c[quarter * 2 + mt], a, bl[ks][0], bl[ks][1]);
+      mma_16816(c[quarter * 2 + mt], z, bh[ks][0], bh[ks][1]);
+    }
+  }
+}
+
+// A lane's 8 levels (hi in the low halves, remainders in the high ones) as one
+// 16-byte chunk of its tile row.
+template <bool kRest>
+__device__ __forceinline__ void store_levels(uint32_t addr, const uint32_t (&hv)[8]) {
+  constexpr uint32_t sel = kRest ? 0x7632 : 0x5410;
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(__byte_perm(hv[0], hv[1], sel)),
+               "r"(__byte_perm(hv[2], hv[3], sel)), "r"(__byte_perm(hv[4], hv[5], sel)),
+               "r"(__byte_perm(hv[6], hv[7], sel))
+               : "memory");
+}
+
 // Online-softmax update for one group's scores (lane = token); keeps the
 // probabilities p (without the V norm) in `p` for the caller.
 template <int G>
@@ -359,7 +397,7 @@ __global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const DecodeArgs
 // enough registers for its larger accumulators.
 __host__ __device__ constexpr int max_warps_for(int G) { return G >= 8 ? 12 : kMaxWarps; }
 
-template <int G, bool kTwoK, bool kTwoV, bool kWin>
+template <int G, bool kTwoK, bool kTwoV, bool kWin, bool kLo>
 __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int nwarps = blockDim.x >> 5;
@@ -587,15 +625,18 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
       const uint32_t *lev16 = reinterpret_cast<const uint32_t *>(lev + kMaxLevels);
-      auto run_half = [&](auto half_c) {
-        constexpr int half = decltype(half_c)::value;
+      // kCoords coordinates go through the tile at a time: 64 levels, or 32
+      // and their remainders (kLo).
+      constexpr int kCoords = kLo ? kHalf / 2 : kHalf;
+      auto run_part = [&](auto part_c) {
+        constexpr int part = decltype(part_c)::value;
 #pragma unroll 1
-        for (int i8 = 0; i8 < kHalf; i8 += 8) {
+        for (int i8 = 0; i8 < kCoords; i8 += 8) {
           uint32_t hv[8];
           if (has_next) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              const int i = half * kHalf + i8 + u;
+              const int i = part * kCoords + i8 + u;
               const uint32_t ek = rans_step<kTwoK>(rk, lut_k, smem);
               const uint32_t ev = rans_step<kTwoV>(rv, lut_v, smem);
               const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + ek);
@@ -609,18 +650,20 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
               hv[u] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev16) + ev);
             }
           }
-          const uint4 pk = make_uint4(__byte_perm(hv[0], hv[1], 0x5410), __byte_perm(hv[2], hv[3], 0x5410),
-                                      __byte_perm(hv[4], hv[5], 0x5410), __byte_perm(hv[6], hv[7], 0x5410));
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(tile_s + tile_off(lane, i8 >> 3)),
-                       "r"(pk.x), "r"(pk.y), "r"(pk.z), "r"(pk.w)
-                       : "memory");
+          store_levels<false>(tile_s + tile_off(lane, i8 >> 3), hv);
+          if constexpr (kLo) store_levels<true>(tile_s + tile_off(lane, 4 + (i8 >> 3)), hv);
         }
         __syncwarp();
-        pv_mma_half<half>(acc.c, tile_s, fb_hi, fb_lo, lane);
+        if constexpr (kLo) pv_mma_quarter<part>(acc.c, tile_s, fb_hi, fb_lo, lane);
+        else pv_mma_half<part>(acc.c, tile_s, fb_hi, fb_lo, lane);
         __syncwarp();
       };
-      run_half(std::integral_constant<int, 0>{});
-      run_half(std::integral_constant<int, 1>{});
+      run_part(std::integral_constant<int, 0>{});
+      run_part(std::integral_constant<int, 1>{});
+      if constexpr (kLo) {
+        run_part(std::integral_constant<int, 2>{});
+        run_part(std::integral_constant<int, 3>{});
+      }
       {
         const bool vvalid = visible(group_t0(j));
         count_bad(vvalid, rv, vb);
@@ -779,37 +822,37 @@ int warps_for(int G, int ck, int cv) {
   return nw;
 }
 
-template <int G, bool kTwoK, bool kTwoV, bool kWin>
+template <int G, bool kTwoK, bool kTwoV, bool kWin, bool kLo>
 int launch_split(const DecodeArgs &a, cudaStream_t st) {
   const int nw = warps_for(G, a.ck, a.cv);
   if (static_cast<int64_t>(a.grid) * nw != a.total_warps) return static_cast<int>(cudaErrorInvalidValue);
   const SplitSmem L = split_smem_layout(G, a.ck, a.cv, nw);
-  constexpr auto kern = decode_split_kernel<G, kTwoK, kTwoV, kWin>;
+  constexpr auto kern = decode_split_kernel<G, kTwoK, kTwoV, kWin, kLo>;
   const cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
   if (e != cudaSuccess) return static_cast<int>(e);
   kern<<<a.grid, nw * 32, L.total, st>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
 
-template <int G, bool kWin>
+template <int G, bool kWin, bool kLo>
 int launch_split_g(const DecodeArgs &a, cudaStream_t st) {
-  if (a.two_k && a.two_v) return launch_split<G, true, true, kWin>(a, st);
-  if (a.two_k) return launch_split<G, true, false, kWin>(a, st);
-  if (a.two_v) return launch_split<G, false, true, kWin>(a, st);
-  return launch_split<G, false, false, kWin>(a, st);
+  if (a.two_k && a.two_v) return launch_split<G, true, true, kWin, kLo>(a, st);
+  if (a.two_k) return launch_split<G, true, false, kWin, kLo>(a, st);
+  if (a.two_v) return launch_split<G, false, true, kWin, kLo>(a, st);
+  return launch_split<G, false, false, kWin, kLo>(a, st);
 }
 
 // Prefix and split kernels.
-template <bool kWin>
+template <bool kWin, bool kLo>
 int launch_groups(const DecodeArgs &a, cudaStream_t st) {
   prefix_kernel<kWin><<<1, kPrefixThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return static_cast<int>(e);
   switch (a.G) {
-    case 1: return launch_split_g<1, kWin>(a, st);
-    case 2: return launch_split_g<2, kWin>(a, st);
-    case 4: return launch_split_g<4, kWin>(a, st);
-    case 8: return launch_split_g<8, kWin>(a, st);
+    case 1: return launch_split_g<1, kWin, kLo>(a, st);
+    case 2: return launch_split_g<2, kWin, kLo>(a, st);
+    case 4: return launch_split_g<4, kWin, kLo>(a, st);
+    case 8: return launch_split_g<8, kWin, kLo>(a, st);
     default: return static_cast<int>(cudaErrorInvalidValue);
   }
 }
@@ -825,7 +868,9 @@ int decode_warps_per_cta(int G, int ck, int cv) {
 int launch_decode_attention(const DecodeArgs &a, void *stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.ck > kMaxContainer || a.cv > kMaxContainer || a.grid < 1) return static_cast<int>(cudaErrorInvalidValue);
-  const int e = a.window > 0 ? launch_groups<true>(a, st) : launch_groups<false>(a, st);
+  const int e = a.window == 0 ? launch_groups<false, false>(a, st)
+                : a.out_dtype == DQ_F32 ? launch_groups<true, true>(a, st)
+                                        : launch_groups<true, false>(a, st);
   if (e) return e;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
   if (rows > 0x7FFFFFFF) return static_cast<int>(cudaErrorInvalidValue);

@@ -49,8 +49,9 @@ struct alignas(16) DevStream {
   float cost[kMaxLevels];
   uint32_t freq[kMaxLevels];
   uint32_t cum[kMaxLevels];
-  // Levels for fp16 tensor-core operands: level16[s] holds the fp16 bits of
-  // tile_scale * levels[s]; tile_scale in [1, 2) is chosen on the host so that
+  // Levels for fp16 tensor-core operands: the low half of level16[s] holds the
+  // fp16 bits of tile_scale * levels[s], the high half those of what the low
+  // one leaves (the sum is exact to 2^-22); tile_scale in [1, 2) is chosen on the host so that
   // these fp16 values are as close as possible (relatively) to the scaled
   // fp32 levels; tile_rel_err is the largest relative error left.
   uint32_t level16[kMaxLevels];

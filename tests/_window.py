@@ -8,7 +8,8 @@ with, a logit is off by at most d = 140 * 2^-24 A + scale * sum |q~_i dy_i| ||k|
 then off by a factor of at most exp(2 d). P.V adds the relative error e_v of
 V's levels, the fp32 sums over n tokens (n + 64) 2^-24, the weights' and the
 exponential's 2^-20 in all, and (chunks) the fp16 halves' smallest step 2^-25
-per token times the largest level. Rotations keep the 2-norm, so each output
+per token times the largest level. fp32 outputs of a decode step carry V's
+levels in two fp16 parts, so e_v is 2^-22 there (the second part's rounding). Rotations keep the 2-norm, so each output
 coordinate is off by at most the sum of these times the largest visible ||v||.
 """
 from __future__ import annotations
@@ -33,7 +34,7 @@ def level_errors(stream, frequency_weighted):
     return err[j]
 
 
-def attention(tab, q, kcont, vcont, start, window, sinks, chunk, sm_scale=None):
+def attention(tab, q, kcont, vcont, start, window, sinks, chunk, sm_scale=None, half_levels=True):
     """q [B, n, Hq, 128]; flat containers [B, Hkv, T_cap, C]; query i of
     sequence b at position start[b] + i (a position outside the cache gives 0).
     Returns (out, bound) with bound [B, n, Hq, 1]."""
@@ -44,6 +45,8 @@ def attention(tab, q, kcont, vcont, start, window, sinks, chunk, sm_scale=None):
     scale = 1.0 / math.sqrt(128.0) if sm_scale is None else sm_scale
     dk = level_errors(tab.k, True) if chunk else np.zeros(len(tab.k.yf))
     ev = float((level_errors(tab.v, False) / np.abs(tab.v.yf.astype(np.float64))).max())
+    if not half_levels:
+        ev = 2.0 ** -22
     H = o.hadamard(128)
     out, bound = np.zeros((B, n, Hq, 128)), np.zeros((B, n, Hq, 1))
     for b in range(B):

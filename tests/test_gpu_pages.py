@@ -209,7 +209,7 @@ def test_argument_errors(tab):
         dq.dq_pages_compact(tab, r, t, r, t, pairs, c, ws)
     with pytest.raises(ValueError, match="lens"):
         dq.dq_pages_advance(tab, r, t, L.long(), n, *outs, c, ws)
-    with pytest.raises(ValueError, match="kpool"):
+    with pytest.raises(ValueError, match="pools"):
         dq.dq_pages_copy(tab, dq.new_pool(8, 3, 36), dq.new_pool(8, 2, 36), pairs)
 
 

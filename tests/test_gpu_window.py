@@ -23,10 +23,10 @@ pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 
 
-def _setup(B, Hkv, G, T, bits=2.26, seed_name="qwen3_8b_b16_t8k"):
-    w = synth.scaled(synth.WORKLOADS[seed_name], B=B, Hkv=Hkv, Hq=Hkv * G, T=T)
+def _setup(B, Hkv, G, T, bits=2.26, v_levels=6):
+    w = synth.scaled(synth.WORKLOADS["qwen3_8b_b16_t8k"], B=B, Hkv=Hkv, Hq=Hkv * G, T=T)
     K, V, _ = cm.inputs(w)
-    lib, ref = cm.lib_tables(Hkv, bits, bits), cm.oracle_tables(Hkv, bits, bits)
+    lib, ref = cm.lib_tables(Hkv, bits, bits, v_levels=v_levels), cm.oracle_tables(Hkv, bits, bits, v_levels=v_levels)
     kc, vc = cm.gpu_append_all(lib, K, V, BF16)
     return w, lib, ref, kc, vc, cm.flat(kc), cm.flat(vc)
 
@@ -67,7 +67,7 @@ def test_decode_matches_definition(window, sinks):
     q = synth.q_block(w)
     stats = dq.new_stats()
     got = _np(_decode(lib, q, kc, vc, lens, window, sinks, stats=stats))
-    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, window, sinks, chunk=False)
+    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, window, sinks, chunk=False, half_levels=False)
     W.assert_within(got, want[:, 0], bound[:, 0], False, "window %d sinks %d" % (window, sinks))
     assert np.all(got[1] == 0.0)
     s = dq.stats_dict(stats)
@@ -81,8 +81,21 @@ def test_decode_group_sizes_and_types(G, bits, dtype):
     lens, window, sinks = [500, 411, 130, 17], 129, 6
     q = _rounded(synth.q_block(w), dtype)
     got = _np(_decode(lib, q, kc, vc, lens, window, sinks, dtype=dtype))
-    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, window, sinks, chunk=False)
+    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, window, sinks, chunk=False,
+                              half_levels=dtype == BF16)
     W.assert_within(got, want[:, 0], bound[:, 0], dtype == BF16, "G %d" % G)
+
+
+@pytest.mark.parametrize("v_levels,bits", [(2, 2.26), (4, 1.96), (8, 1.96), (8, 2.26), (8, 3.0)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decode_value_tables_of_every_size(v_levels, bits, dtype):
+    B, Hkv, G, T = 3, 2, 2, 400
+    w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T, bits, v_levels)
+    lens, q, stats = [400, 300, 90], _rounded(synth.q_block(w), dtype), dq.new_stats()
+    got = _np(_decode(lib, q, kc, vc, lens, 150, 5, dtype=dtype, stats=stats))
+    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, 150, 5, chunk=False, half_levels=dtype == BF16)
+    W.assert_within(got, want[:, 0], bound[:, 0], dtype == BF16, "%d levels" % v_levels)
+    assert dq.stats_dict(stats)["integrity_errors"] == 0
 
 
 def test_decode_many_sequences_and_a_scale():
@@ -92,17 +105,20 @@ def test_decode_many_sequences_and_a_scale():
     lens = [(b * 7) % 65 for b in range(B)]
     q = synth.q_block(w)
     got = _np(_decode(lib, q, kc, vc, lens, 20, 2, sm_scale=0.25))
-    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, 20, 2, chunk=False, sm_scale=0.25)
+    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, 20, 2, chunk=False, sm_scale=0.25, half_levels=False)
     W.assert_within(got, want[:, 0], bound[:, 0], False, "1500 sequences")
 
 
 def test_decode_window_of_everything_is_the_call_without_one():
     B, Hkv, G, T = 3, 2, 4, 333
-    w, lib, ref, kc, vc, _, _ = _setup(B, Hkv, G, T)
+    w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T)
     lens, q = [333, 100, 0], synth.q_block(w)
-    full = cm.gpu_attention(lib, q, kc, vc, lens, T_max=kc.shape[2])
+    qr = _rounded(q, BF16)
+    half = cm.gpu_attention(lib, qr, kc, vc, lens, T_max=kc.shape[2], q_dtype=BF16, out_dtype=BF16)
+    want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, 333, 0, chunk=False, half_levels=False)
     for window, sinks in ((333, 0), (2 ** 40, 0), (1, 333), (200, 2 ** 40)):
-        assert np.array_equal(_np(_decode(lib, q, kc, vc, lens, window, sinks)), full)
+        assert np.array_equal(_np(_decode(lib, qr, kc, vc, lens, window, sinks, dtype=BF16)), half)
+        W.assert_within(_np(_decode(lib, q, kc, vc, lens, window, sinks)), want[:, 0], bound[:, 0], False, "everything")
 
 
 def _pool_of(lib, cache, table, num_pages, keep):

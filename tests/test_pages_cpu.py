@@ -40,9 +40,9 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(ValueError, match="CUDA"):
         dq.dq_pages_advance(None, r, t, L, L, r, t, L, r, r)
     with pytest.raises(ValueError, match="refs"):
-        N._check_int32(refs=(r, (9,)))
+        N._check_int32("lens refs", (L, (2,)), (r, (9,)))
     with pytest.raises(ValueError, match="lens"):
-        N._check_int32(lens=(L.long(), (2,)))
+        N._check_int32("lens", (L.long(), (2,)))
 
 
 @pytest.mark.parametrize("seed", range(6))

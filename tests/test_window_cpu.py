@@ -56,13 +56,15 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
 
 
 def test_binding_refuses_shapes_that_do_not_fit():
-    N._check_lens("seq_lens", torch.zeros(3, dtype=torch.int32), 3)
+    N._check_int32("seq_lens", (torch.zeros(3, dtype=torch.int32), (3,)))
     for bad in (torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64), torch.zeros(3, 1, dtype=torch.int32)):
         with pytest.raises(ValueError, match="seq_lens"):
-            N._check_lens("seq_lens", bad, 3)
+            N._check_int32("seq_lens", (bad, (3,)))
     q = torch.zeros(1, 4, 128)
     cache = torch.zeros(1, 1, 32, 36, dtype=torch.uint8)
     for args in ((torch.zeros(1, 4, 64), torch.zeros(1, 4, 64), cache, cache), (q, q[:, :2], cache, cache),
-                 (q, q, cache.float(), cache), (q, q, cache, cache[:, :, :16].repeat(2, 1, 1, 1))):
+                 (q, q, cache.float(), cache), (q, q, cache, cache.int())):
         with pytest.raises(ValueError):
-            N._check_heads(None, *args)
+            N._check_heads(*args)
+    with pytest.raises(ValueError, match="caches"):
+        N._check_shapes("caches", cache, cache[:, :, :16], (1, 1, 32, 36), (1, 1, 32, 36))
