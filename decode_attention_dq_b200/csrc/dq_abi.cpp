@@ -646,7 +646,7 @@ static int prefill_core(const dq_tables *t, const void *q, int q_dtype, const ui
       a.bh0 = bh0;
       a.nbh = std::min<int64_t>(per_wave, rows - bh0);
       const int64_t groups = a.nbh * std::min<int64_t>(T_cap / 32, a.row_slots * 4);
-      a.tile_grid = static_cast<int>(std::min<int64_t>(t->sm_count, (groups + 19) / 20));
+      a.tile_grid = static_cast<int>(std::min<int64_t>(t->sm_count, window > 0 ? groups : (groups + 19) / 20));
       int e = dqi::launch_prefill_attention(a, stream);
       if (e != 0) return cuda_fail(static_cast<cudaError_t>(e));
     }

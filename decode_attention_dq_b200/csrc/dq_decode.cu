@@ -50,9 +50,13 @@
 // of each sequence the groups of the first tokens, then those from the
 // window's first token on. Nothing else changes: the hidden groups take no
 // place in the order, their bytes and page-table entries are never read.
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "dq_device.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace dqi {
 namespace {
@@ -319,6 +323,34 @@ __device__ __forceinline__ float finite_norm_of(const uint8_t *cb) {
   return (cb[kTile] & 0x7C) == 0x7C ? 0.0f : norm_of(cb);
 }
 
+// A group's weights w = p ||v|| (lane = token) as fp16 hi + lo through the
+// weight buffer, then this lane's B fragments: b[ks][0] holds tokens 16 ks + 2
+// (lane % 4) + {0, 1} of head lane / 4, b[ks][1] the same tokens + 8 (zero for
+// heads >= G).
+template <int G>
+__device__ __forceinline__ void weight_fragments(const float (&p)[G], float nv, bool valid, uint16_t *wh,
+                                                 uint32_t (&hi)[2][2], uint32_t (&lo)[2][2], int lane) {
+#pragma unroll
+  for (int gg = 0; gg < G; ++gg) {
+    const float w = valid ? p[gg] * nv : 0.0f;
+    const __half wh_hi = __float2half_rn(w);
+    const __half wh_lo = __float2half_rn(w - __half2float(wh_hi));
+    wh[gg * kWhStride + lane] = __half_as_ushort(wh_hi);
+    wh[(8 + gg) * kWhStride + lane] = __half_as_ushort(wh_lo);
+  }
+  __syncwarp();
+  const uint32_t *whw = reinterpret_cast<const uint32_t *>(wh);
+  const int n_head = lane >> 2, cq = lane & 3;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int word = n_head * (kWhStride / 2) + ks * 8 + r * 4 + cq;
+      hi[ks][r] = n_head < G ? whw[word] : 0u;
+      lo[ks][r] = n_head < G ? whw[8 * (kWhStride / 2) + word] : 0u;
+    }
+}
+
 __device__ __forceinline__ int64_t clamp_len(int32_t len, int64_t cap) {
   int64_t v = len;
   if (v < 0) v = 0;
@@ -411,7 +443,6 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
   uint8_t *vst = wsm + L.vst;
   const uint32_t tile_s = static_cast<uint32_t>(__cvta_generic_to_shared(wsm + L.tile));
   uint16_t *wh = reinterpret_cast<uint16_t *>(wsm + L.wbuf);  // [hi, lo][8 heads][kWhStride]
-  const uint32_t *whw = reinterpret_cast<const uint32_t *>(wh);
   float *qt = reinterpret_cast<float *>(wsm + L.qt);  // [128][G]
   const int ck = a.ck, cv = a.cv;
 
@@ -438,7 +469,10 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
   // Warps that take part: all of them, or one per group when there are
   // fewer groups than warps, so that no participating warp is empty.
   const int64_t W = active_warps(static_cast<int64_t>(gridDim.x) * nwarps, N);
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * nwarps + warp;
+  // (With a window there are often fewer groups than warps: neighbouring
+  // ranges then go to different SMs.)
+  const int64_t wid = kWin ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
+                           : static_cast<int64_t>(blockIdx.x) * nwarps + warp;
   if (wid >= W) return;
   int64_t g = warp_first(wid, W, N);
   const int64_t g_end = warp_first(wid + 1, W, N);
@@ -583,33 +617,12 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
     for (int64_t j = 0; j < n; ++j) {
       const int cur = static_cast<int>(j & 1), nxt = cur ^ 1;
       const bool has_next = j + 1 < n;
-      // V(j) is in slot cur, K(j+1) in slot nxt (both staged). Weights of
-      // group j, w = p ||v||, as fp16 hi + lo, then this lane's B fragments:
-      // b[ks][0] holds tokens 16 ks + 2 (lane % 4) + {0, 1} of head lane / 4,
-      // b[ks][1] the same tokens + 8 (zero for heads >= G).
+      // V(j) is in slot cur, K(j+1) in slot nxt (both staged).
       uint32_t fb_hi[2][2], fb_lo[2][2];
       {
         const uint8_t *vb = vst + cur * kTile * cv + lane;
         const bool valid = visible(group_t0(j));
-        const float nv = norm_at(vb);
-#pragma unroll
-        for (int gg = 0; gg < G; ++gg) {
-          const float w = valid ? p[gg] * nv : 0.0f;
-          const __half hi = __float2half_rn(w);
-          const __half lo = __float2half_rn(w - __half2float(hi));
-          wh[gg * kWhStride + lane] = __half_as_ushort(hi);
-          wh[(8 + gg) * kWhStride + lane] = __half_as_ushort(lo);
-        }
-        __syncwarp();
-        const int n_head = lane >> 2, cq = lane & 3;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int word = n_head * (kWhStride / 2) + ks * 8 + r * 4 + cq;
-            fb_hi[ks][r] = n_head < G ? whw[word] : 0u;
-            fb_lo[ks][r] = n_head < G ? whw[8 * (kWhStride / 2) + word] : 0u;
-          }
+        weight_fragments<G>(p, norm_at(vb), valid, wh, fb_hi, fb_lo, lane);
       }
       // Prefetch K(j+2) into slot cur and V(j+1) into slot nxt.
       if (j + 2 < n) stage_block(kst + cur * kTile * ck, kblock(bj2), ck, lane);
@@ -816,6 +829,233 @@ __global__ void __launch_bounds__(kCombWarps * 32) combine_kernel(const DecodeAr
   }
 }
 
+// Few groups: a window bounds the groups of a (b, h) on the host, and where
+// they are so few that every one can have a warp of its own, the time of a
+// call is the latency of one chain of 128 symbols plus what comes before and
+// after it. One cluster of CTAs per (b, h) then does the whole call in one
+// launch: warp w of CTA r takes visible group w C + r, decodes its K and its V
+// side by side (the whole V tile stays in shared memory until the weights are
+// known), the CTAs merge their warps' states, and the cluster merges the CTAs'
+// through distributed shared memory, a query head per CTA.
+constexpr int kFewWarps = 12;      // most warps per CTA
+constexpr int kFewCluster = 16;    // most CTAs per cluster
+
+struct FewSmem {
+  size_t lut_k, lut_v, lev, qt, ml, cta_ml, cta_o, warp0, kst, vst, tile, wbuf, warp_bytes, total;
+};
+
+__host__ __device__ inline FewSmem few_smem_layout(int G, int ck, int cv, bool lo, int nwarps) {
+  FewSmem s;
+  s.lut_k = 0;
+  s.lut_v = s.lut_k + kM * 4;
+  s.lev = s.lut_v + kM * 4;
+  s.qt = align16(s.lev + 2 * kMaxLevels * 4);                       // [128][G] floats
+  s.ml = s.qt + static_cast<size_t>(kD) * G * 4;                    // [warps][G] (max, sum)
+  s.cta_ml = s.ml + align16(static_cast<size_t>(kFewWarps) * G * 8);  // [G] (max, sum) of the CTA
+  s.cta_o = s.cta_ml + align16(static_cast<size_t>(G) * 8);         // [G][128] of the CTA
+  s.warp0 = s.cta_o + static_cast<size_t>(G) * kD * 4;
+  s.kst = 0;
+  s.vst = align16(static_cast<size_t>(kTile) * ck);
+  // The tile in parts of 32 tokens x 128 bytes: two halves of the
+  // coordinates, or four quarters with their remainders; then o [G][128].
+  s.tile = s.vst + align16(static_cast<size_t>(kTile) * cv);
+  s.wbuf = s.tile + static_cast<size_t>(lo ? 4 : 2) * kTile * kTileRow;
+  s.warp_bytes = align16(s.wbuf + 2 * 8 * kWhStride * 2);
+  // (A corrupt container's cursor runs at most 2 bytes per symbol past byte
+  // 5, see split_smem_layout.)
+  const size_t reach = s.vst + static_cast<size_t>(kTile) * (kHeaderBytes + 2 * kD + 1);
+  const size_t slack = reach > s.warp_bytes ? align16(reach - s.warp_bytes) : 0;
+  s.total = s.warp0 + static_cast<size_t>(nwarps) * s.warp_bytes + slack + 256;
+  return s;
+}
+
+template <int G, bool kTwo, bool kLo>
+__global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  cg::cluster_group cl = cg::this_cluster();
+  const int nwarps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
+  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, nwarps);
+  uint32_t *lut_k = reinterpret_cast<uint32_t *>(smem + L.lut_k);
+  uint32_t *lut_v = reinterpret_cast<uint32_t *>(smem + L.lut_v);
+  float *lev = reinterpret_cast<float *>(smem + L.lev);
+  float *qt = reinterpret_cast<float *>(smem + L.qt);
+  float2 *ml = reinterpret_cast<float2 *>(smem + L.ml);
+  float2 *cta_ml = reinterpret_cast<float2 *>(smem + L.cta_ml);
+  float *cta_o = reinterpret_cast<float *>(smem + L.cta_o);
+  uint8_t *wsm = smem + L.warp0 + warp * L.warp_bytes;
+  const int64_t bh = blockIdx.x / C;
+  const int b = static_cast<int>(bh / a.Hkv), h = static_cast<int>(bh % a.Hkv);
+
+  // This warp's group: its containers are on their way before anything else.
+  const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap;
+  const int32_t raw = a.seq_lens[b];
+  const int64_t len = clamp_len(raw, cap);
+  const WindowSpan span = visible_groups<true>(a, len);
+  const int64_t j = static_cast<int64_t>(warp) * C + rank;
+  const bool mine = j < span.n;
+  const int64_t tb = span.block(j);
+  unsigned bad_pages = 0;
+  if (mine) {
+    int64_t blk = bh * (a.T_cap / kTile) + tb;
+    if (a.page_table) {
+      int64_t pg = a.page_table[static_cast<int64_t>(b) * a.max_pages + tb];
+      if (pg < 0 || pg >= a.num_pages) {
+        bad_pages = 1;
+        pg = 0;
+      }
+      blk = pg * a.Hkv + h;
+    }
+    stage_block(wsm + L.kst, a.kcache + blk * kTile * a.ck, a.ck, lane);
+    stage_block(wsm + L.vst, a.vcache + blk * kTile * a.cv, a.cv, lane);
+  }
+  for (int i = threadIdx.x; i < static_cast<int>(kM / 4); i += blockDim.x) {
+    cp_async16(reinterpret_cast<uint4 *>(lut_k) + i, reinterpret_cast<const uint4 *>(a.tabs->k.lut) + i);
+    cp_async16(reinterpret_cast<uint4 *>(lut_v) + i, reinterpret_cast<const uint4 *>(a.tabs->v.lut) + i);
+  }
+  cp_async_commit();
+  if (threadIdx.x < kMaxLevels) {
+    lev[threadIdx.x] = a.tabs->k.levels[threadIdx.x];
+    reinterpret_cast<uint32_t *>(lev)[kMaxLevels + threadIdx.x] = a.tabs->v.level16[threadIdx.x];
+  }
+  // D1, a head per warp.
+  for (int gg = warp; gg < G; gg += nwarps) {
+    const float qscale = a.sm_scale * kLog2e / static_cast<float>(kD);
+    const int64_t qbase = (static_cast<int64_t>(b) * a.Hq + h * G + gg) * kD;
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = apply_sign(load_elem(a.q, qbase + lane + 32 * k, a.q_dtype), __ldg(a.sign_bits + h * 4 + k), lane);
+    wht128_warp(v, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) qt[(lane + 32 * k) * G + gg] = v[k] * qscale;
+  }
+  cp_async_wait_0();
+  __syncthreads();
+
+  unsigned bad_count = 0, over_count = 0;
+  if (mine) {
+    const uint8_t *kb = wsm + L.kst + lane, *vb = wsm + L.vst + lane;
+    const uint32_t tile_s = static_cast<uint32_t>(__cvta_generic_to_shared(wsm + L.tile));
+    const uint32_t *lev16 = reinterpret_cast<const uint32_t *>(lev + kMaxLevels);
+    RansLane rk = rans_open(smem, static_cast<uint32_t>(kb - smem));
+    RansLane rv = rans_open(smem, static_cast<uint32_t>(vb - smem));
+    float sc[G];
+#pragma unroll
+    for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
+#pragma unroll 1
+    for (int i8 = 0; i8 < kD; i8 += 8) {
+      uint32_t hv[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t ek = rans_step<kTwo>(rk, lut_k, smem);
+        const uint32_t ev = rans_step<kTwo>(rv, lut_v, smem);
+        const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + ek);
+        hv[u] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev16) + ev);
+        score_fma<G>(sc, qt + (i8 + u) * G, yk);
+      }
+      constexpr int kCoords = kLo ? kHalf / 2 : kHalf;
+      const uint32_t part = tile_s + (i8 / kCoords) * (kTile * kTileRow);
+      const int chunk = (i8 % kCoords) >> 3;
+      store_levels<false>(part + tile_off(lane, chunk), hv);
+      if constexpr (kLo) store_levels<true>(part + tile_off(lane, 4 + chunk), hv);
+    }
+    const int64_t t = tb * kTile + lane;
+    const bool valid = t < len && (t < a.sinks || t >= len - a.window);
+    const bool bad_k = rk.x != kL || (kb[kTile] & 0x7C) == 0x7C, bad_v = rv.x != kL || (vb[kTile] & 0x7C) == 0x7C;
+    bad_count = __popc(__ballot_sync(kFull, valid && bad_k)) + __popc(__ballot_sync(kFull, valid && bad_v));
+#ifdef DQ_CHECKED
+    over_count = __popc(__ballot_sync(kFull, valid && overread(rk, kb, smem, a.ck))) +
+                 __popc(__ballot_sync(kFull, valid && overread(rv, vb, smem, a.cv)));
+#endif
+    WarpAcc<G> acc;
+#pragma unroll
+    for (int gg = 0; gg < G; ++gg) {
+      acc.m[gg] = -INFINITY;
+      acc.l[gg] = 0.0f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc.c[mt][e] = 0.0f;
+    float p[G];
+    softmax_update(acc, sc, finite_norm_of(kb), valid, p, lane);
+    uint32_t fb_hi[2][2], fb_lo[2][2];
+    weight_fragments<G>(p, finite_norm_of(vb), valid, reinterpret_cast<uint16_t *>(wsm + L.wbuf), fb_hi, fb_lo, lane);
+    constexpr int kPart = kTile * kTileRow;
+    if constexpr (kLo) {
+      pv_mma_quarter<0>(acc.c, tile_s, fb_hi, fb_lo, lane);
+      pv_mma_quarter<1>(acc.c, tile_s + kPart, fb_hi, fb_lo, lane);
+      pv_mma_quarter<2>(acc.c, tile_s + 2 * kPart, fb_hi, fb_lo, lane);
+      pv_mma_quarter<3>(acc.c, tile_s + 3 * kPart, fb_hi, fb_lo, lane);
+    } else {
+      pv_mma_half<0>(acc.c, tile_s, fb_hi, fb_lo, lane);
+      pv_mma_half<1>(acc.c, tile_s + kPart, fb_hi, fb_lo, lane);
+    }
+    __syncwarp();  // the tile has been read: o takes its place
+    float *o = reinterpret_cast<float *>(wsm + L.tile);
+    const int row = lane >> 2, head0 = 2 * (lane & 3);
+#pragma unroll
+    for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (head0 + (e & 1) < G) o[(head0 + (e & 1)) * kD + 16 * mt + row + 8 * (e >> 1)] = acc.c[mt][e];
+    if (lane == 0)
+#pragma unroll
+      for (int gg = 0; gg < G; ++gg) ml[warp * G + gg] = make_float2(acc.m[gg], acc.l[gg]);
+  } else if (lane < G) {
+    ml[warp * G + lane] = make_float2(-INFINITY, 0.0f);
+  }
+  __syncthreads();
+
+  // D7 in the CTA: a warp with no group (or no visible token) weighs nothing.
+  for (int i = threadIdx.x; i < G * kD; i += blockDim.x) {
+    const int gg = i / kD;
+    float M = -INFINITY, l = 0.0f, o = 0.0f;
+    for (int w = 0; w < nwarps; ++w) M = fmaxf(M, ml[w * G + gg].x);
+    if (M != -INFINITY)
+      for (int w = 0; w < nwarps; ++w) {
+        const float2 s = ml[w * G + gg];
+        if (s.x == -INFINITY) continue;
+        const float r = exp2f(s.x - M);
+        l = fmaf(r, s.y, l);
+        o = fmaf(r, reinterpret_cast<const float *>(smem + L.warp0 + w * L.warp_bytes + L.tile)[i], o);
+      }
+    cta_o[i] = o;
+    if (i % kD == 0) cta_ml[gg] = make_float2(M, l);
+  }
+  cl.sync();
+
+  // D7 in the cluster: head gg belongs to CTA gg % C.
+  for (int gg = rank + C * warp; gg < G; gg += C * nwarps) {
+    const float2 s = lane < C ? cl.map_shared_rank(cta_ml, lane)[gg] : make_float2(-INFINITY, 0.0f);
+    const float M = warp_max(s.x);
+    const float r = M == -INFINITY ? 0.0f : exp2f(s.x - M);
+    const float l = warp_sum(r * s.y);
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int c = 0; c < C; ++c) {
+      const float rc = __shfl_sync(kFull, r, c);
+      const float *src = cl.map_shared_rank(cta_o, c) + gg * kD + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(rc, src[32 * k], o[k]);
+    }
+    const float inv = l > 0.0f ? 1.0f / (l * static_cast<float>(kD) * a.tabs->v.tile_scale) : 0.0f;
+    wht128_warp(o, lane);
+    const int64_t row = static_cast<int64_t>(b) * a.Hq + h * G + gg;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      store_elem(a.out, row * kD + lane + 32 * k, apply_sign(o[k] * inv, __ldg(a.sign_bits + h * 4 + k), lane), a.out_dtype);
+  }
+  if (a.stats && lane == 0) {
+    if (bad_count) atomicAdd(&a.stats->integrity_errors, static_cast<unsigned long long>(bad_count));
+    if (bad_pages) atomicAdd(&a.stats->bad_pages, static_cast<unsigned long long>(bad_pages));
+    if (over_count) atomicAdd(&a.stats->overreads, static_cast<unsigned long long>(over_count));
+    if (warp == 0 && rank == 0 && h == 0 && raw != len) atomicAdd(&a.stats->clamped_lengths, 1ull);
+  }
+  cl.sync();  // the other CTAs have read this one's state
+}
+
 int warps_for(int G, int ck, int cv) {
   int nw = max_warps_for(G);
   while (nw > 1 && split_smem_layout(G, ck, cv, nw).total > 227 * 1024) --nw;
@@ -857,6 +1097,62 @@ int launch_groups(const DecodeArgs &a, cudaStream_t st) {
   }
 }
 
+// Launch shape of decode_few_kernel, cluster 0 where it does not serve: the
+// most CTAs per (b, KV head) that the SMs hold at once, and a warp per group.
+struct FewShape {
+  int cluster, warps;
+};
+
+FewShape few_shape(const DecodeArgs &a) {
+  FewShape s{0, 0};
+  const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap, all = (cap + kTile - 1) / kTile;
+  const int64_t seen = (a.sinks + kTile - 1) / kTile + (a.window + kTile - 2) / kTile + 1;
+  const int64_t groups = seen < all ? seen : all;  // at most, of one (b, h)
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
+  if (a.window == 0 || rows > a.grid) return s;
+  int C = kFewCluster;
+  while (C > 1 && (rows * C > a.grid || C / 2 >= groups)) C /= 2;
+  const int64_t nw = groups > C ? (groups + C - 1) / C : 1;
+  if (nw > kFewWarps || few_smem_layout(a.G, a.ck, a.cv, a.out_dtype == DQ_F32, static_cast<int>(nw)).total > 227 * 1024)
+    return s;
+  s.cluster = C;
+  s.warps = static_cast<int>(nw);
+  return s;
+}
+
+template <int G, bool kTwo, bool kLo>
+int launch_few(const DecodeArgs &a, FewShape f, cudaStream_t st) {
+  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, f.warps);
+  constexpr auto kern = decode_few_kernel<G, kTwo, kLo>;
+  cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
+  if (e == cudaSuccess) e = allow_wide_cluster<kern>();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hkv * f.cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(f.warps * 32));
+  cfg.dynamicSmemBytes = L.total;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(f.cluster);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+template <bool kTwo, bool kLo>
+int launch_few_g(const DecodeArgs &a, FewShape f, cudaStream_t st) {
+  switch (a.G) {
+    case 1: return launch_few<1, kTwo, kLo>(a, f, st);
+    case 2: return launch_few<2, kTwo, kLo>(a, f, st);
+    case 4: return launch_few<4, kTwo, kLo>(a, f, st);
+    case 8: return launch_few<8, kTwo, kLo>(a, f, st);
+    default: return static_cast<int>(cudaErrorInvalidValue);
+  }
+}
+
 }  // namespace
 
 int decode_warps_per_cta(int G, int ck, int cv) {
@@ -868,6 +1164,11 @@ int decode_warps_per_cta(int G, int ck, int cv) {
 int launch_decode_attention(const DecodeArgs &a, void *stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.ck > kMaxContainer || a.cv > kMaxContainer || a.grid < 1) return static_cast<int>(cudaErrorInvalidValue);
+  if (const FewShape f = few_shape(a); f.cluster > 0) {
+    const bool two = a.two_k || a.two_v, lo = a.out_dtype == DQ_F32;
+    if (two) return lo ? launch_few_g<true, true>(a, f, st) : launch_few_g<true, false>(a, f, st);
+    return lo ? launch_few_g<false, true>(a, f, st) : launch_few_g<false, false>(a, f, st);
+  }
   const int e = a.window == 0 ? launch_groups<false, false>(a, st)
                 : a.out_dtype == DQ_F32 ? launch_groups<true, true>(a, st)
                                         : launch_groups<true, false>(a, st);

@@ -531,7 +531,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
     for (int c = lane; c < (kGrp * cv) >> 4; c += 32) cp_async16(vslot(sl) + c * 16, vs + c * 16);
   };
 
-  int64_t u = next_valid(static_cast<int64_t>(blockIdx.x) * kTileWarps + warp);
+  // (With a window there are often fewer units than warps: neighbouring ones
+  // then go to different SMs.)
+  int64_t u = next_valid(kWin ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
+                              : static_cast<int64_t>(blockIdx.x) * kTileWarps + warp);
   if (u < total && decoded(u)) stage(0, u);
   cp_async_commit();
   for (int k = 0; u < total; ++k) {

@@ -60,10 +60,11 @@ def _np(t):
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 4), (32, 32), (33, 0), (64, 31), (100, 33), (250, 64),
                                           (257, 5), (1000, 3), (7, 1000)])
-def test_decode_matches_definition(window, sinks):
-    B, Hkv, G, T = 9, 2, 4, 300
+@pytest.mark.parametrize("times", [1, 11])  # one cluster per (b, h), and more rows than there are SMs
+def test_decode_matches_definition(window, sinks, times):
+    B, Hkv, G, T = 9 * times, 2, 4, 300
     w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T)
-    lens = [300, 0, 1, 31, 32, 33, 64, 97, 255]
+    lens = [300, 0, 1, 31, 32, 33, 64, 97, 255] * times
     q = synth.q_block(w)
     stats = dq.new_stats()
     got = _np(_decode(lib, q, kc, vc, lens, window, sinks, stats=stats))
@@ -75,10 +76,11 @@ def test_decode_matches_definition(window, sinks):
 
 
 @pytest.mark.parametrize("G,bits,dtype", [(1, 1.96, F32), (2, 2.26, BF16), (8, 3.0, F32), (8, 2.26, BF16), (4, 3.0, BF16)])
-def test_decode_group_sizes_and_types(G, bits, dtype):
-    B, Hkv, T = 4, 2, 500
+@pytest.mark.parametrize("times", [1, 20])
+def test_decode_group_sizes_and_types(G, bits, dtype, times):
+    B, Hkv, T = 4 * times, 2, 500
     w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T, bits)
-    lens, window, sinks = [500, 411, 130, 17], 129, 6
+    lens, window, sinks = [500, 411, 130, 17] * times, 129, 6
     q = _rounded(synth.q_block(w), dtype)
     got = _np(_decode(lib, q, kc, vc, lens, window, sinks, dtype=dtype))
     want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, window, sinks, chunk=False,
@@ -88,14 +90,26 @@ def test_decode_group_sizes_and_types(G, bits, dtype):
 
 @pytest.mark.parametrize("v_levels,bits", [(2, 2.26), (4, 1.96), (8, 1.96), (8, 2.26), (8, 3.0)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_decode_value_tables_of_every_size(v_levels, bits, dtype):
-    B, Hkv, G, T = 3, 2, 2, 400
+@pytest.mark.parametrize("times", [1, 30])
+def test_decode_value_tables_of_every_size(v_levels, bits, dtype, times):
+    B, Hkv, G, T = 3 * times, 2, 2, 400
     w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T, bits, v_levels)
-    lens, q, stats = [400, 300, 90], _rounded(synth.q_block(w), dtype), dq.new_stats()
+    lens, q, stats = [400, 300, 90] * times, _rounded(synth.q_block(w), dtype), dq.new_stats()
     got = _np(_decode(lib, q, kc, vc, lens, 150, 5, dtype=dtype, stats=stats))
     want, bound = W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, 150, 5, chunk=False, half_levels=dtype == BF16)
     W.assert_within(got, want[:, 0], bound[:, 0], dtype == BF16, "%d levels" % v_levels)
     assert dq.stats_dict(stats)["integrity_errors"] == 0
+
+
+@pytest.mark.parametrize("T", [1500, 3100, 6300])
+def test_decode_long_windows(T):
+    # One head: 47, 97 and 197 groups, i.e. 3 and 7 warps per CTA of a 16-CTA cluster, then the balanced split.
+    w, lib, ref, kc, vc, rk, rv = _setup(1, 1, 4, T)
+    q = synth.q_block(w)
+    for window, sinks in ((T - 40, 7), (T // 2, 64)):
+        got = _np(_decode(lib, q, kc, vc, [T], window, sinks))
+        want, bound = W.attention(ref, q[:, None], rk, rv, [T - 1], window, sinks, chunk=False, half_levels=False)
+        W.assert_within(got, want[:, 0], bound[:, 0], False, "T %d window %d" % (T, window))
 
 
 def test_decode_many_sequences_and_a_scale():
@@ -145,10 +159,11 @@ def _paged(lib, kc, vc, lens, n_q, window, sinks, seed):
 
 
 @pytest.mark.parametrize("window,sinks", [(40, 0), (65, 5), (128, 64)])
-def test_decode_paged_reads_only_what_is_visible(window, sinks):
-    B, Hkv, G, T = 4, 3, 2, 400
+@pytest.mark.parametrize("times", [1, 13])
+def test_decode_paged_reads_only_what_is_visible(window, sinks, times):
+    B, Hkv, G, T = 4 * times, 3, 2, 400
     w, lib, ref, kc, vc, _, _ = _setup(B, Hkv, G, T)
-    lens, q = [400, 385, 66, 7], synth.q_block(w)
+    lens, q = [400, 385, 66, 7] * times, synth.q_block(w)
     want = _decode(lib, q, kc, vc, lens, window, sinks)
     kp, vp, table = _paged(lib, kc, vc, lens, 1, window, sinks, 3)
     stats = dq.new_stats()
@@ -160,10 +175,11 @@ def test_decode_paged_reads_only_what_is_visible(window, sinks):
     assert s["bad_pages"] == 0 and s["integrity_errors"] == 0
 
 
-def test_decode_hidden_and_later_tokens_may_be_garbage():
-    B, Hkv, G, T = 2, 2, 4, 320
+@pytest.mark.parametrize("times", [1, 40])
+def test_decode_hidden_and_later_tokens_may_be_garbage(times):
+    B, Hkv, G, T = 2 * times, 2, 4, 320
     w, lib, ref, kc, vc, _, _ = _setup(B, Hkv, G, T)
-    lens, window, sinks, q = [290, 155], 70, 3, synth.q_block(w)
+    lens, window, sinks, q = [290, 155] * times, 70, 3, synth.q_block(w)
     want = _decode(lib, q, kc, vc, lens, window, sinks)
     for c in (kc, vc):
         blocks = c.reshape(B, Hkv, T // 32, c.shape[3], 32)
@@ -176,19 +192,21 @@ def test_decode_hidden_and_later_tokens_may_be_garbage():
     assert dq.stats_dict(stats)["integrity_errors"] == 0
 
 
-def test_decode_counts_visible_corrupt_containers_and_long_lengths():
-    B, Hkv, G, T = 2, 1, 2, 96
+@pytest.mark.parametrize("rows", [2, 160])
+def test_decode_counts_visible_corrupt_containers_and_long_lengths(rows):
+    B, Hkv, G, T = rows, 1, 2, 96
     w, lib, ref, kc, vc, _, _ = _setup(B, Hkv, G, T)
     q = synth.q_block(w)
-    want = _decode(lib, q, kc, vc, [96, 96], 30, 2)
+    rest = [50] * (rows - 2)
+    want = _decode(lib, q, kc, vc, [96, 96] + rest, 30, 2)
     for t in (95, 40, 1):  # two visible ones, one hidden
         vc.reshape(B, Hkv, 3, 36, 32)[0, :, t // 32, 0:2, t % 32] = 0xFF
     stats = dq.new_stats()
-    got = _decode(lib, q, kc, vc, [2000, -5], 30, 2, stats=stats)
+    got = _decode(lib, q, kc, vc, [2000, -5] + rest, 30, 2, stats=stats)
     assert torch.isfinite(got).all() and torch.all(got[1] == 0)
     s = dq.stats_dict(stats)
     assert s["integrity_errors"] == 2 and s["clamped_lengths"] == 2
-    assert torch.equal(_decode(lib, q, kc, vc, [96, 96], 30, 2)[1], want[1])
+    assert torch.equal(_decode(lib, q, kc, vc, [96, 96] + rest, 30, 2)[1:], want[1:])
 
 
 def _prefill(lib, q, kc, vc, start, window, sinks, q_dtype=F32, out_dtype=F32, stats=None, workspace=None):
