@@ -379,6 +379,15 @@ __host__ __device__ __forceinline__ int64_t warp_first(int64_t w, int64_t W, int
 // w owns exactly group w.
 __host__ __device__ __forceinline__ int64_t active_warps(int64_t total, int64_t N) { return total < N ? total : N; }
 
+// With a window, so many that each gets the same whole number of groups (but
+// for the last ones): with about two groups per warp a few warps with one
+// more would run a last pass alone.
+__host__ __device__ __forceinline__ int64_t active_warps(int64_t total, int64_t N, bool window) {
+  if (!window || N == 0) return active_warps(total, N);
+  const int64_t each = (N + total - 1) / total;
+  return (N + each - 1) / each;
+}
+
 // Token groups per sequence and their prefix sums: prefix[b] = groups of
 // sequences 0..b-1, prefix[B] = total. One CTA of kPrefixThreads threads;
 // also counts the sequence lengths that had to be clamped.
@@ -468,7 +477,7 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
   const int64_t N = a.prefix[a.B] * Hkv;  // total token groups
   // Warps that take part: all of them, or one per group when there are
   // fewer groups than warps, so that no participating warp is empty.
-  const int64_t W = active_warps(static_cast<int64_t>(gridDim.x) * nwarps, N);
+  const int64_t W = active_warps(static_cast<int64_t>(gridDim.x) * nwarps, N, kWin);
   // (With a window there are often fewer groups than warps: neighbouring
   // ranges then go to different SMs.)
   const int64_t wid = kWin ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
@@ -764,7 +773,7 @@ __global__ void __launch_bounds__(kCombWarps * 32) combine_kernel(const DecodeAr
     // the largest w with first(w) <= g); none of them is empty (W <= N), and
     // each wrote its partial state of (b, h) to slot bh + w.
     const int64_t N = a.prefix[a.B] * Hkv;
-    const int64_t W = active_warps(a.total_warps, N);
+    const int64_t W = active_warps(a.total_warps, N, a.window > 0);
     const int64_t g0 = a.prefix[b] * Hkv + h * gb, g1 = g0 + gb;
     const int64_t w_lo = ((g0 + 1) * W - 1) / N;
     const int64_t w_hi = (g1 * W - 1) / N;
