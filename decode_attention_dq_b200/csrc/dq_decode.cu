@@ -150,8 +150,7 @@ __device__ __forceinline__ bool overread(const RansLane &r, const uint8_t *cb, c
 // (x >= 16 f after the step); kTwo enables that step for tables that have
 // such a symbol. The byte reads never
 // leave the kernel's shared memory (the cursor moves at most 2 bytes per
-// symbol and the layout leaves room for that). Returns the byte offset 4 s
-// of the symbol's level.
+// symbol and the layout leaves room for that). Returns the table entry.
 template <bool kTwo>
 __device__ __forceinline__ uint32_t rans_step(RansLane &r, const uint32_t *lut, const uint8_t *smem) {
   const uint32_t e = lut[r.x & (kM - 1)];
@@ -169,8 +168,11 @@ __device__ __forceinline__ uint32_t rans_step(RansLane &r, const uint32_t *lut, 
   }
   r.p = p;
   r.x = x;
-  return (e >> 9) & 0x1Cu;
+  return e;
 }
+
+// Byte offset 4 s of the symbol's fp32 level.
+__device__ __forceinline__ uint32_t level_offset(uint32_t e) { return (e >> 9) & 0x1Cu; }
 
 // fp16 norm in bytes 0 and 1 of a staged (interleaved) container.
 __device__ __forceinline__ float norm_of(const uint8_t *cb) {
@@ -269,15 +271,18 @@ __device__ __forceinline__ void pv_mma_quarter(float (&c)[kD / 16][4], uint32_t 
   }
 }
 
-// A lane's 8 levels (hi in the low halves, remainders in the high ones) as one
-// 16-byte chunk of its tile row.
-template <bool kRest>
-__device__ __forceinline__ void store_levels(uint32_t addr, const uint32_t (&hv)[8]) {
-  constexpr uint32_t sel = kRest ? 0x7632 : 0x5410;
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(__byte_perm(hv[0], hv[1], sel)),
-               "r"(__byte_perm(hv[2], hv[3], sel)), "r"(__byte_perm(hv[4], hv[5], sel)),
-               "r"(__byte_perm(hv[6], hv[7], sel))
-               : "memory");
+// A lane's 8 levels (of the entries' symbols) as one 16-byte chunk of its tile
+// row at `hi`, with kLo their remainders at `lo`.
+template <bool kLo>
+__device__ __forceinline__ void store_levels(uint32_t hi, uint32_t lo, const uint32_t (&e)[8], const LevelPool &th,
+                                             const LevelPool &tl) {
+  const uint32_t s0 = symbol_selector(e[0], e[1], e[2], e[3]), s1 = symbol_selector(e[4], e[5], e[6], e[7]);
+  const uint2 a = pool_levels(th, s0), b = pool_levels(th, s1);
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(hi), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
+  if constexpr (kLo) {
+    const uint2 c = pool_levels(tl, s0), d = pool_levels(tl, s1);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(lo), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
+  }
 }
 
 // Online-softmax update for one group's scores (lane = token); keeps the
@@ -395,6 +400,7 @@ constexpr int kPrefixThreads = 1024;
 
 template <bool kWin>
 __global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const DecodeArgs a) {
+  if constexpr (kWin) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ int64_t warp_tot[kPrefixThreads / 32];
   __shared__ int64_t carry_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
   const SplitSmem L = split_smem_layout(G, a.ck, a.cv, nwarps);
   uint32_t *lut_k = reinterpret_cast<uint32_t *>(smem + L.lut_k);
   uint32_t *lut_v = reinterpret_cast<uint32_t *>(smem + L.lut_v);
-  float *lev = reinterpret_cast<float *>(smem + L.lev);  // [0..7] K levels, [8..15] V fp16 bits
+  float *lev = reinterpret_cast<float *>(smem + L.lev);  // K levels
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t *wsm = smem + L.warp0 + warp * L.warp_bytes;
   uint8_t *kst = wsm + L.kst;
@@ -465,12 +471,13 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
       dk[i] = __ldg(sk + i);
       dv[i] = __ldg(sv + i);
     }
-    if (threadIdx.x < kMaxLevels) {
-      lev[threadIdx.x] = a.tabs->k.levels[threadIdx.x];
-      reinterpret_cast<uint32_t *>(lev)[kMaxLevels + threadIdx.x] = a.tabs->v.level16[threadIdx.x];
-    }
+    if (threadIdx.x < kMaxLevels) lev[threadIdx.x] = a.tabs->k.levels[threadIdx.x];
   }
+  const LevelPool pool_hi = level_pool(a.tabs->v.level16, 0), pool_lo = level_pool(a.tabs->v.level16, 16);
   __syncthreads();
+  // Windowed calls launch the three kernels so that one may start while the
+  // one before it runs (launch_after): what it wrote is complete from here on.
+  if constexpr (kWin) asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap;
   const int64_t Hkv = a.Hkv;
@@ -480,6 +487,7 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
   const int64_t W = active_warps(static_cast<int64_t>(gridDim.x) * nwarps, N, kWin);
   // (With a window there are often fewer groups than warps: neighbouring
   // ranges then go to different SMs.)
+  if constexpr (kWin) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int64_t wid = kWin ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
                            : static_cast<int64_t>(blockIdx.x) * nwarps + warp;
   if (wid >= W) return;
@@ -613,7 +621,7 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
 #pragma unroll 4
       for (int i = 0; i < kD; ++i) {
         const uint32_t ek = rans_step<kTwoK>(rk, lut_k, smem);
-        const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + ek);
+        const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(ek));
         score_fma<G>(sc, qt + i * G, yk);
       }
       const bool valid = visible(group_t0(0));
@@ -646,7 +654,6 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
       RansLane rv = rans_open(smem, static_cast<uint32_t>(vb - smem));
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
-      const uint32_t *lev16 = reinterpret_cast<const uint32_t *>(lev + kMaxLevels);
       // kCoords coordinates go through the tile at a time: 64 levels, or 32
       // and their remainders (kLo).
       constexpr int kCoords = kLo ? kHalf / 2 : kHalf;
@@ -660,20 +667,17 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
             for (int u = 0; u < 8; ++u) {
               const int i = part * kCoords + i8 + u;
               const uint32_t ek = rans_step<kTwoK>(rk, lut_k, smem);
-              const uint32_t ev = rans_step<kTwoV>(rv, lut_v, smem);
-              const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + ek);
-              hv[u] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev16) + ev);
+              hv[u] = rans_step<kTwoV>(rv, lut_v, smem);
+              const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(ek));
               score_fma<G>(sc, qt + i * G, yk);
             }
           } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              const uint32_t ev = rans_step<kTwoV>(rv, lut_v, smem);
-              hv[u] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev16) + ev);
+              hv[u] = rans_step<kTwoV>(rv, lut_v, smem);
             }
           }
-          store_levels<false>(tile_s + tile_off(lane, i8 >> 3), hv);
-          if constexpr (kLo) store_levels<true>(tile_s + tile_off(lane, 4 + (i8 >> 3)), hv);
+          store_levels<kLo>(tile_s + tile_off(lane, i8 >> 3), tile_s + tile_off(lane, 4 + (i8 >> 3)), hv, pool_hi, pool_lo);
         }
         __syncwarp();
         if constexpr (kLo) pv_mma_quarter<part>(acc.c, tile_s, fb_hi, fb_lo, lane);
@@ -753,8 +757,9 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
 // small batch a row has hundreds of slots (one per split warp) and few rows
 // run at once, so the host takes 16 warps per CTA there (the merge is a
 // chain of load batches, latency-bound), 4 otherwise.
-template <int kCombWarps>
+template <int kCombWarps, bool kWin>
 __global__ void __launch_bounds__(kCombWarps * 32) combine_kernel(const DecodeArgs a) {
+  if constexpr (kWin) asm volatile("griddepcontrol.wait;\n" ::: "memory");
   __shared__ float sh_m[kCombWarps], sh_l[kCombWarps];
   __shared__ float sh_o[kCombWarps][kD];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -773,7 +778,7 @@ __global__ void __launch_bounds__(kCombWarps * 32) combine_kernel(const DecodeAr
     // the largest w with first(w) <= g); none of them is empty (W <= N), and
     // each wrote its partial state of (b, h) to slot bh + w.
     const int64_t N = a.prefix[a.B] * Hkv;
-    const int64_t W = active_warps(a.total_warps, N, a.window > 0);
+    const int64_t W = active_warps(a.total_warps, N, kWin);
     const int64_t g0 = a.prefix[b] * Hkv + h * gb, g1 = g0 + gb;
     const int64_t w_lo = ((g0 + 1) * W - 1) / N;
     const int64_t w_hi = (g1 * W - 1) / N;
@@ -923,10 +928,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
     cp_async16(reinterpret_cast<uint4 *>(lut_v) + i, reinterpret_cast<const uint4 *>(a.tabs->v.lut) + i);
   }
   cp_async_commit();
-  if (threadIdx.x < kMaxLevels) {
-    lev[threadIdx.x] = a.tabs->k.levels[threadIdx.x];
-    reinterpret_cast<uint32_t *>(lev)[kMaxLevels + threadIdx.x] = a.tabs->v.level16[threadIdx.x];
-  }
+  if (threadIdx.x < kMaxLevels) lev[threadIdx.x] = a.tabs->k.levels[threadIdx.x];
   // D1, a head per warp.
   for (int gg = warp; gg < G; gg += nwarps) {
     const float qscale = a.sm_scale * kLog2e / static_cast<float>(kD);
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
   if (mine) {
     const uint8_t *kb = wsm + L.kst + lane, *vb = wsm + L.vst + lane;
     const uint32_t tile_s = static_cast<uint32_t>(__cvta_generic_to_shared(wsm + L.tile));
-    const uint32_t *lev16 = reinterpret_cast<const uint32_t *>(lev + kMaxLevels);
+    const LevelPool pool_hi = level_pool(a.tabs->v.level16, 0), pool_lo = level_pool(a.tabs->v.level16, 16);
     RansLane rk = rans_open(smem, static_cast<uint32_t>(kb - smem));
     RansLane rv = rans_open(smem, static_cast<uint32_t>(vb - smem));
     float sc[G];
@@ -958,16 +960,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const uint32_t ek = rans_step<kTwo>(rk, lut_k, smem);
-        const uint32_t ev = rans_step<kTwo>(rv, lut_v, smem);
-        const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + ek);
-        hv[u] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev16) + ev);
+        hv[u] = rans_step<kTwo>(rv, lut_v, smem);
+        const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(ek));
         score_fma<G>(sc, qt + (i8 + u) * G, yk);
       }
       constexpr int kCoords = kLo ? kHalf / 2 : kHalf;
       const uint32_t part = tile_s + (i8 / kCoords) * (kTile * kTileRow);
       const int chunk = (i8 % kCoords) >> 3;
-      store_levels<false>(part + tile_off(lane, chunk), hv);
-      if constexpr (kLo) store_levels<true>(part + tile_off(lane, 4 + chunk), hv);
+      store_levels<kLo>(part + tile_off(lane, chunk), part + tile_off(lane, 4 + chunk), hv, pool_hi, pool_lo);
     }
     const int64_t t = tb * kTile + lane;
     const bool valid = t < len && (t < a.sinks || t >= len - a.window);
@@ -1071,6 +1071,24 @@ int warps_for(int G, int ck, int cv) {
   return nw;
 }
 
+// Launches Kern so that it may start before the kernel in front of it has
+// ended (it waits for that kernel's results itself): its launch and its set-up
+// then overlap that kernel.
+template <auto Kern>
+int launch_after(const DecodeArgs &a, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, Kern, a));
+}
+
 template <int G, bool kTwoK, bool kTwoV, bool kWin, bool kLo>
 int launch_split(const DecodeArgs &a, cudaStream_t st) {
   const int nw = warps_for(G, a.ck, a.cv);
@@ -1079,6 +1097,7 @@ int launch_split(const DecodeArgs &a, cudaStream_t st) {
   constexpr auto kern = decode_split_kernel<G, kTwoK, kTwoV, kWin, kLo>;
   const cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
   if (e != cudaSuccess) return static_cast<int>(e);
+  if constexpr (kWin) return launch_after<kern>(a, static_cast<unsigned>(a.grid), static_cast<unsigned>(nw * 32), L.total, st);
   kern<<<a.grid, nw * 32, L.total, st>>>(a);
   return static_cast<int>(cudaGetLastError());
 }
@@ -1104,6 +1123,13 @@ int launch_groups(const DecodeArgs &a, cudaStream_t st) {
     case 8: return launch_split_g<8, kWin, kLo>(a, st);
     default: return static_cast<int>(cudaErrorInvalidValue);
   }
+}
+
+template <int kCombWarps>
+int launch_combine(const DecodeArgs &a, unsigned rows, cudaStream_t st) {
+  if (a.window > 0) return launch_after<combine_kernel<kCombWarps, true>>(a, rows, kCombWarps * 32, 0, st);
+  combine_kernel<kCombWarps, false><<<rows, kCombWarps * 32, 0, st>>>(a);
+  return static_cast<int>(cudaGetLastError());
 }
 
 // Launch shape of decode_few_kernel, cluster 0 where it does not serve: the
@@ -1186,10 +1212,8 @@ int launch_decode_attention(const DecodeArgs &a, void *stream) {
   if (rows > 0x7FFFFFFF) return static_cast<int>(cudaErrorInvalidValue);
   // At least 64 slots per (b, KV head) possible: wide CTAs.
   if (a.total_warps >= static_cast<int64_t>(64) * a.B * a.Hkv)
-    combine_kernel<16><<<static_cast<unsigned>(rows), 16 * 32, 0, st>>>(a);
-  else
-    combine_kernel<4><<<static_cast<unsigned>(rows), 4 * 32, 0, st>>>(a);
-  return static_cast<int>(cudaGetLastError());
+    return launch_combine<16>(a, static_cast<unsigned>(rows), st);
+  return launch_combine<4>(a, static_cast<unsigned>(rows), st);
 }
 
 }  // namespace dqi

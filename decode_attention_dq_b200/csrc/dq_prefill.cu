@@ -108,15 +108,14 @@ __host__ __device__ inline size_t align_up(size_t v, size_t a) { return (v + a -
 // Shared memory of prefill_tiles_kernel: decode tables, then per warp two
 // staging slots for K and two for V.
 struct TilesSmem {
-  size_t lut_k, lut_v, lev, stage, kslot, vslot, stage_bytes, total;
+  size_t lut_k, lut_v, stage, kslot, vslot, stage_bytes, total;
 };
 
 __host__ __device__ inline TilesSmem tiles_smem_layout(int ck, int cv) {
   TilesSmem s;
   s.lut_k = 0;
   s.lut_v = s.lut_k + kM * 4;
-  s.lev = s.lut_v + kM * 4;  // [0..7] K score levels, [8..15] V tile levels (fp16 bits)
-  s.stage = align_up(s.lev + 2 * kMaxLevels * 4, 128);
+  s.stage = align_up(s.lut_v + kM * 4, 128);
   s.kslot = align_up(static_cast<size_t>(kGrp) * ck, 16);
   s.vslot = align_up(static_cast<size_t>(kGrp) * cv, 16);
   s.stage_bytes = 2 * s.kslot + 2 * s.vslot;
@@ -414,7 +413,7 @@ __device__ __forceinline__ RansLane rans_open(const uint8_t *smem, uint32_t off)
 
 // One decode step (table entry: bits 0..10 slot - c_s, 11..13 s, 20..31 f_s):
 // x = f (x >> 12) + slot - c_s, then byte renormalisation by selects (one
-// byte, or two for tables with a symbol of f < 16). Returns 4 s.
+// byte, or two for tables with a symbol of f < 16). Returns the table entry.
 template <bool kTwo>
 __device__ __forceinline__ uint32_t rans_step(RansLane &r, const uint32_t *lut, const uint8_t *smem) {
   const uint32_t e = lut[r.x & (kM - 1)];
@@ -432,7 +431,7 @@ __device__ __forceinline__ uint32_t rans_step(RansLane &r, const uint32_t *lut, 
   }
   r.p = p;
   r.x = x;
-  return (e >> 9) & 0x1Cu;
+  return e;
 }
 
 __device__ __forceinline__ float norm_of(const uint8_t *cb) {
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t *lut_k = reinterpret_cast<uint32_t *>(smem + L.lut_k);
   uint32_t *lut_v = reinterpret_cast<uint32_t *>(smem + L.lut_v);
-  uint32_t *lev = reinterpret_cast<uint32_t *>(smem + L.lev);
+  const LevelPool pool_k = level_pool(a.tabs->k.score16, 0), pool_v = level_pool(a.tabs->v.level16, 0);
   {
     const uint4 *sk = reinterpret_cast<const uint4 *>(a.tabs->k.lut);
     const uint4 *sv = reinterpret_cast<const uint4 *>(a.tabs->v.lut);
@@ -459,13 +458,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
       dk[i] = __ldg(sk + i);
       dv[i] = __ldg(sv + i);
     }
-    if (threadIdx.x < kMaxLevels) {
-      lev[threadIdx.x] = a.tabs->k.score16[threadIdx.x];
-      lev[kMaxLevels + threadIdx.x] = a.tabs->v.level16[threadIdx.x];
-    }
   }
   __syncthreads();
 
+  if constexpr (kWin) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int ck = a.ck, cv = a.cv;
   const int64_t gslots = kWin ? a.row_slots : (a.T_cap + kBlk - 1) / kBlk;  // slots per (b, h)
   constexpr int kQuarters = kBlk / kGrp;
@@ -558,19 +554,17 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) prefill_tiles_kernel(const
         uint32_t hk[8], hv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint32_t ek = rans_step<kTwoK>(rk, lut_k, smem);
-          const uint32_t ev = rans_step<kTwoV>(rv, lut_v, smem);
-          hk[e] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev) + ek);
-          hv[e] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(lev) + 4 * kMaxLevels + ev);
+          hk[e] = rans_step<kTwoK>(rk, lut_k, smem);
+          hv[e] = rans_step<kTwoV>(rv, lut_v, smem);
         }
         // 8 coordinates of this lane's token: 16 bytes in chunk i8 / 8.
         const size_t off = static_cast<size_t>((i8 >> 3) * kChunkStride + tl * 16);
-        *reinterpret_cast<uint4 *>(dst + off) =
-            make_uint4(__byte_perm(hk[0], hk[1], 0x5410), __byte_perm(hk[2], hk[3], 0x5410),
-                       __byte_perm(hk[4], hk[5], 0x5410), __byte_perm(hk[6], hk[7], 0x5410));
-        *reinterpret_cast<uint4 *>(dst + kTileBytes + off) =
-            make_uint4(__byte_perm(hv[0], hv[1], 0x5410), __byte_perm(hv[2], hv[3], 0x5410),
-                       __byte_perm(hv[4], hv[5], 0x5410), __byte_perm(hv[6], hv[7], 0x5410));
+        const uint2 k0 = pool_levels(pool_k, symbol_selector(hk[0], hk[1], hk[2], hk[3]));
+        const uint2 k1 = pool_levels(pool_k, symbol_selector(hk[4], hk[5], hk[6], hk[7]));
+        const uint2 v0 = pool_levels(pool_v, symbol_selector(hv[0], hv[1], hv[2], hv[3]));
+        const uint2 v1 = pool_levels(pool_v, symbol_selector(hv[4], hv[5], hv[6], hv[7]));
+        *reinterpret_cast<uint4 *>(dst + off) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+        *reinterpret_cast<uint4 *>(dst + kTileBytes + off) = make_uint4(v0.x, v0.y, v1.x, v1.y);
       }
       // Tokens that no row attends to keep zero norms: their bytes may be
       // anything, and the softmax multiplies the weights by them. (kWin: nor
@@ -1153,6 +1147,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
     }
   } else if (warp == kLoadWarp) {
     // ===== slot loader (one lane) =====
+    // (kWin: launched while the tile kernel may still run; its slots are
+    // complete from here on, and only this warp reads them.)
+    if constexpr (kWin) asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (lane == 0 && nB > 0) {
       const uint8_t *src = a.tiles + static_cast<size_t>((bh - a.bh0) * gslots) * kSlotBytes;
       // Workspace slot of a block: the row's slots are those of the whole
@@ -1234,8 +1231,24 @@ int launch_wave(const PrefillArgs &a, unsigned grid, cudaStream_t st) {
   const AttnSmem L = attn_smem_layout(a.nslots);
   const cudaError_t ce = ensure_max_dynamic_smem<prefill_kernel<kWin>>(static_cast<int>(L.total));
   if (ce != cudaSuccess) return static_cast<int>(ce);
-  prefill_kernel<kWin><<<grid, kAttnThreads, L.total, st>>>(a);
-  return static_cast<int>(cudaGetLastError());
+  if constexpr (kWin) {
+    // The attention kernel may start while the tile kernel runs: its loader
+    // waits for the tiles, the query rotations come before.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = L.total;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, prefill_kernel<kWin>, a));
+  } else {
+    prefill_kernel<kWin><<<grid, kAttnThreads, L.total, st>>>(a);
+    return static_cast<int>(cudaGetLastError());
+  }
 }
 
 }  // namespace
