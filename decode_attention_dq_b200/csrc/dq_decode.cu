@@ -328,22 +328,18 @@ __device__ __forceinline__ float finite_norm_of(const uint8_t *cb) {
   return (cb[kTile] & 0x7C) == 0x7C ? 0.0f : norm_of(cb);
 }
 
-// A group's weights w = p ||v|| (lane = token) as fp16 hi + lo through the
-// weight buffer, then this lane's B fragments: b[ks][0] holds tokens 16 ks + 2
+// A token's weight w = p ||v|| for head gg as fp16 hi + lo in the weight buffer.
+__device__ __forceinline__ void store_weight(uint16_t *wh, int gg, int lane, float w) {
+  const __half hi = __float2half_rn(w);
+  const __half lo = __float2half_rn(w - __half2float(hi));
+  wh[gg * kWhStride + lane] = __half_as_ushort(hi);
+  wh[(8 + gg) * kWhStride + lane] = __half_as_ushort(lo);
+}
+// This lane's B fragments of a group's weights: b[ks][0] holds tokens 16 ks + 2
 // (lane % 4) + {0, 1} of head lane / 4, b[ks][1] the same tokens + 8 (zero for
 // heads >= G).
 template <int G>
-__device__ __forceinline__ void weight_fragments(const float (&p)[G], float nv, bool valid, uint16_t *wh,
-                                                 uint32_t (&hi)[2][2], uint32_t (&lo)[2][2], int lane) {
-#pragma unroll
-  for (int gg = 0; gg < G; ++gg) {
-    const float w = valid ? p[gg] * nv : 0.0f;
-    const __half wh_hi = __float2half_rn(w);
-    const __half wh_lo = __float2half_rn(w - __half2float(wh_hi));
-    wh[gg * kWhStride + lane] = __half_as_ushort(wh_hi);
-    wh[(8 + gg) * kWhStride + lane] = __half_as_ushort(wh_lo);
-  }
-  __syncwarp();
+__device__ __forceinline__ void load_weights(const uint16_t *wh, uint32_t (&hi)[2][2], uint32_t (&lo)[2][2], int lane) {
   const uint32_t *whw = reinterpret_cast<const uint32_t *>(wh);
   const int n_head = lane >> 2, cq = lane & 3;
 #pragma unroll
@@ -639,7 +635,11 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
       {
         const uint8_t *vb = vst + cur * kTile * cv + lane;
         const bool valid = visible(group_t0(j));
-        weight_fragments<G>(p, norm_at(vb), valid, wh, fb_hi, fb_lo, lane);
+        const float nv = norm_at(vb);
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) store_weight(wh, gg, lane, valid ? p[gg] * nv : 0.0f);
+        __syncwarp();
+        load_weights<G>(wh, fb_hi, fb_lo, lane);
       }
       // Prefetch K(j+2) into slot cur and V(j+1) into slot nxt.
       if (j + 2 < n) stage_block(kst + cur * kTile * ck, kblock(bj2), ck, lane);
@@ -844,69 +844,95 @@ __global__ void __launch_bounds__(kCombWarps * 32) combine_kernel(const DecodeAr
 }
 
 // Few groups: a window bounds the groups of a (b, h) on the host, and where
-// they are so few that every one can have a warp of its own, the time of a
+// they are so few that every one can have warps of its own, the time of a
 // call is the latency of one chain of 128 symbols plus what comes before and
 // after it. One cluster of CTAs per (b, h) then does the whole call in one
-// launch: warp w of CTA r takes visible group w C + r, decodes its K and its V
-// side by side (the whole V tile stays in shared memory until the weights are
-// known), the CTAs merge their warps' states, and the cluster merges the CTAs'
-// through distributed shared memory, a query head per CTA.
-constexpr int kFewWarps = 12;      // most warps per CTA
-constexpr int kFewCluster = 16;    // most CTAs per cluster
+// launch. Group pair w of CTA r takes visible group w C + r: one warp decodes
+// its K and forms the weights, another one decodes its V at the same time
+// (the whole V tile stays in shared memory until the weights are there) and
+// multiplies. (Both chains in one warp took 133 cycles per symbol, a chain
+// alone takes 97.) The CTAs merge their groups' states and store them straight
+// into the shared memory of the CTA that owns the query head, which merges
+// the cluster's after one barrier.
+constexpr int kFewGroups = 12;   // most groups per CTA
+constexpr int kFewCluster = 16;  // most CTAs per cluster
 
 struct FewSmem {
-  size_t lut_k, lut_v, lev, qt, ml, cta_ml, cta_o, warp0, kst, vst, tile, wbuf, warp_bytes, total;
+  size_t bar, lut_k, lut_v, lev, qt, ml, own_ml, own_o, group0, kst, vst, tile, wbuf, group_bytes, total;
 };
 
-__host__ __device__ inline FewSmem few_smem_layout(int G, int ck, int cv, bool lo, int nwarps) {
+// Query heads that a CTA of a cluster of C owns.
+__host__ __device__ constexpr int few_heads(int G, int C) { return (G + C - 1) / C; }
+
+__host__ __device__ inline FewSmem few_smem_layout(int G, int ck, int cv, bool lo, int groups, int C) {
   FewSmem s;
-  s.lut_k = 0;
+  const size_t owned = static_cast<size_t>(few_heads(G, C)) * C;  // states that arrive: per owned head one of each CTA
+  s.bar = 0;
+  s.lut_k = 16;
   s.lut_v = s.lut_k + kM * 4;
   s.lev = s.lut_v + kM * 4;
-  s.qt = align16(s.lev + 2 * kMaxLevels * 4);                       // [128][G] floats
-  s.ml = s.qt + static_cast<size_t>(kD) * G * 4;                    // [warps][G] (max, sum)
-  s.cta_ml = s.ml + align16(static_cast<size_t>(kFewWarps) * G * 8);  // [G] (max, sum) of the CTA
-  s.cta_o = s.cta_ml + align16(static_cast<size_t>(G) * 8);         // [G][128] of the CTA
-  s.warp0 = s.cta_o + static_cast<size_t>(G) * kD * 4;
+  s.qt = align16(s.lev + kMaxLevels * 4);                           // [128][G] floats
+  s.ml = s.qt + static_cast<size_t>(kD) * G * 4;                    // [groups][G] (max, sum)
+  s.own_ml = s.ml + align16(static_cast<size_t>(groups) * G * 8);   // [owned heads][C] (max, sum)
+  s.own_o = s.own_ml + align16(owned * 8);                          // [owned heads][C][128]
+  s.group0 = s.own_o + owned * kD * 4;
   s.kst = 0;
   s.vst = align16(static_cast<size_t>(kTile) * ck);
   // The tile in parts of 32 tokens x 128 bytes: two halves of the
   // coordinates, or four quarters with their remainders; then o [G][128].
   s.tile = s.vst + align16(static_cast<size_t>(kTile) * cv);
   s.wbuf = s.tile + static_cast<size_t>(lo ? 4 : 2) * kTile * kTileRow;
-  s.warp_bytes = align16(s.wbuf + 2 * 8 * kWhStride * 2);
+  s.group_bytes = align16(s.wbuf + 2 * 8 * kWhStride * 2);
   // (A corrupt container's cursor runs at most 2 bytes per symbol past byte
   // 5, see split_smem_layout.)
   const size_t reach = s.vst + static_cast<size_t>(kTile) * (kHeaderBytes + 2 * kD + 1);
-  const size_t slack = reach > s.warp_bytes ? align16(reach - s.warp_bytes) : 0;
-  s.total = s.warp0 + static_cast<size_t>(nwarps) * s.warp_bytes + slack + 256;
+  const size_t slack = reach > s.group_bytes ? align16(reach - s.group_bytes) : 0;
+  s.total = s.group0 + static_cast<size_t>(groups) * s.group_bytes + slack + 256;
   return s;
 }
 
 template <int G, bool kTwo, bool kLo>
-__global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kFewGroups * 64, 1) decode_few_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   cg::cluster_group cl = cg::this_cluster();
-  const int nwarps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = blockDim.x >> 6, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_v = warp >= groups;          // warps 0 .. groups - 1 decode K, the others V
+  const int grp = is_v ? warp - groups : warp;
   const int C = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
-  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, nwarps);
-  uint32_t *lut_k = reinterpret_cast<uint32_t *>(smem + L.lut_k);
-  uint32_t *lut_v = reinterpret_cast<uint32_t *>(smem + L.lut_v);
+  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, groups, C);
+  const uint32_t bar = static_cast<uint32_t>(__cvta_generic_to_shared(smem + L.bar));
+  const uint32_t *lut_k = reinterpret_cast<const uint32_t *>(smem + L.lut_k);
+  const uint32_t *lut_v = reinterpret_cast<const uint32_t *>(smem + L.lut_v);
   float *lev = reinterpret_cast<float *>(smem + L.lev);
   float *qt = reinterpret_cast<float *>(smem + L.qt);
   float2 *ml = reinterpret_cast<float2 *>(smem + L.ml);
-  float2 *cta_ml = reinterpret_cast<float2 *>(smem + L.cta_ml);
-  float *cta_o = reinterpret_cast<float *>(smem + L.cta_o);
-  uint8_t *wsm = smem + L.warp0 + warp * L.warp_bytes;
+  float2 *own_ml = reinterpret_cast<float2 *>(smem + L.own_ml);
+  float *own_o = reinterpret_cast<float *>(smem + L.own_o);
+  uint8_t *gsm = smem + L.group0 + grp * L.group_bytes;
   const int64_t bh = blockIdx.x / C;
   const int b = static_cast<int>(bh / a.Hkv), h = static_cast<int>(bh % a.Hkv);
 
-  // This warp's group: its containers are on their way before anything else.
+  // (Met again before the first store into another CTA: all have started then.)
+  cl.barrier_arrive();
+  // The decode tables, as two bulk copies counted on a barrier.
+  if (threadIdx.x == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(bar) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n" ::"r"(bar), "r"(kM * 8)
+                 : "memory");
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(smem + (t ? L.lut_v : L.lut_k)))),
+                   "l"(t ? a.tabs->v.lut : a.tabs->k.lut), "r"(kM * 4), "r"(bar)
+                   : "memory");
+  }
+  // This warp's containers.
   const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap;
   const int32_t raw = a.seq_lens[b];
   const int64_t len = clamp_len(raw, cap);
   const WindowSpan span = visible_groups<true>(a, len);
-  const int64_t j = static_cast<int64_t>(warp) * C + rank;
+  const int64_t j = static_cast<int64_t>(grp) * C + rank;
   const bool mine = j < span.n;
   const int64_t tb = span.block(j);
   unsigned bad_pages = 0;
@@ -915,22 +941,18 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
     if (a.page_table) {
       int64_t pg = a.page_table[static_cast<int64_t>(b) * a.max_pages + tb];
       if (pg < 0 || pg >= a.num_pages) {
-        bad_pages = 1;
+        bad_pages = is_v ? 0 : 1;
         pg = 0;
       }
       blk = pg * a.Hkv + h;
     }
-    stage_block(wsm + L.kst, a.kcache + blk * kTile * a.ck, a.ck, lane);
-    stage_block(wsm + L.vst, a.vcache + blk * kTile * a.cv, a.cv, lane);
-  }
-  for (int i = threadIdx.x; i < static_cast<int>(kM / 4); i += blockDim.x) {
-    cp_async16(reinterpret_cast<uint4 *>(lut_k) + i, reinterpret_cast<const uint4 *>(a.tabs->k.lut) + i);
-    cp_async16(reinterpret_cast<uint4 *>(lut_v) + i, reinterpret_cast<const uint4 *>(a.tabs->v.lut) + i);
+    if (is_v) stage_block(gsm + L.vst, a.vcache + blk * kTile * a.cv, a.cv, lane);
+    else stage_block(gsm + L.kst, a.kcache + blk * kTile * a.ck, a.ck, lane);
   }
   cp_async_commit();
   if (threadIdx.x < kMaxLevels) lev[threadIdx.x] = a.tabs->k.levels[threadIdx.x];
   // D1, a head per warp.
-  for (int gg = warp; gg < G; gg += nwarps) {
+  for (int gg = warp; gg < G; gg += 2 * groups) {
     const float qscale = a.sm_scale * kLog2e / static_cast<float>(kD);
     const int64_t qbase = (static_cast<int64_t>(b) * a.Hq + h * G + gg) * kD;
     float v[4];
@@ -943,101 +965,122 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
   }
   cp_async_wait_0();
   __syncthreads();
+  // The tables have landed (bounded: a wait that gives up counts, and the
+  // sequence's tokens in this CTA are left out).
+  bool ready = false;
+  for (uint32_t it = 0; it < (1u << 24) && !ready; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred P;\nmbarrier.try_wait.parity.shared::cta.b64 P, [%1], 0;\nselp.u32 %0, 1, 0, P;\n}\n"
+        : "=r"(ok)
+        : "r"(bar)
+        : "memory");
+    ready = ok != 0;
+  }
+  ready = __syncthreads_and(ready);
 
   unsigned bad_count = 0, over_count = 0;
-  if (mine) {
-    const uint8_t *kb = wsm + L.kst + lane, *vb = wsm + L.vst + lane;
-    const uint32_t tile_s = static_cast<uint32_t>(__cvta_generic_to_shared(wsm + L.tile));
-    const LevelPool pool_hi = level_pool(a.tabs->v.level16, 0), pool_lo = level_pool(a.tabs->v.level16, 16);
-    RansLane rk = rans_open(smem, static_cast<uint32_t>(kb - smem));
-    RansLane rv = rans_open(smem, static_cast<uint32_t>(vb - smem));
-    float sc[G];
-#pragma unroll
-    for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
-#pragma unroll 1
-    for (int i8 = 0; i8 < kD; i8 += 8) {
-      uint32_t hv[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t ek = rans_step<kTwo>(rk, lut_k, smem);
-        hv[u] = rans_step<kTwo>(rv, lut_v, smem);
-        const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(ek));
-        score_fma<G>(sc, qt + (i8 + u) * G, yk);
-      }
-      constexpr int kCoords = kLo ? kHalf / 2 : kHalf;
-      const uint32_t part = tile_s + (i8 / kCoords) * (kTile * kTileRow);
-      const int chunk = (i8 % kCoords) >> 3;
-      store_levels<kLo>(part + tile_off(lane, chunk), part + tile_off(lane, 4 + chunk), hv, pool_hi, pool_lo);
-    }
+  if (mine && ready) {
     const int64_t t = tb * kTile + lane;
     const bool valid = t < len && (t < a.sinks || t >= len - a.window);
-    const bool bad_k = rk.x != kL || (kb[kTile] & 0x7C) == 0x7C, bad_v = rv.x != kL || (vb[kTile] & 0x7C) == 0x7C;
-    bad_count = __popc(__ballot_sync(kFull, valid && bad_k)) + __popc(__ballot_sync(kFull, valid && bad_v));
-#ifdef DQ_CHECKED
-    over_count = __popc(__ballot_sync(kFull, valid && overread(rk, kb, smem, a.ck))) +
-                 __popc(__ballot_sync(kFull, valid && overread(rv, vb, smem, a.cv)));
-#endif
-    WarpAcc<G> acc;
+    const uint8_t *cb = gsm + (is_v ? L.vst : L.kst) + lane;
+    RansLane rl = rans_open(smem, static_cast<uint32_t>(cb - smem));
+    uint16_t *wh = reinterpret_cast<uint16_t *>(gsm + L.wbuf);
+    if (!is_v) {
+      float sc[G];
 #pragma unroll
-    for (int gg = 0; gg < G; ++gg) {
-      acc.m[gg] = -INFINITY;
-      acc.l[gg] = 0.0f;
-    }
+      for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
+#pragma unroll 8
+      for (int i = 0; i < kD; ++i) {
+        const uint32_t e = rans_step<kTwo>(rl, lut_k, smem);
+        score_fma<G>(sc, qt + i * G, *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(e)));
+      }
+      const float nk = finite_norm_of(cb), nv = finite_norm_of(gsm + L.vst + lane);
 #pragma unroll
-    for (int mt = 0; mt < kD / 16; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc.c[mt][e] = 0.0f;
-    float p[G];
-    softmax_update(acc, sc, finite_norm_of(kb), valid, p, lane);
-    uint32_t fb_hi[2][2], fb_lo[2][2];
-    weight_fragments<G>(p, finite_norm_of(vb), valid, reinterpret_cast<uint16_t *>(wsm + L.wbuf), fb_hi, fb_lo, lane);
-    constexpr int kPart = kTile * kTileRow;
-    if constexpr (kLo) {
-      pv_mma_quarter<0>(acc.c, tile_s, fb_hi, fb_lo, lane);
-      pv_mma_quarter<1>(acc.c, tile_s + kPart, fb_hi, fb_lo, lane);
-      pv_mma_quarter<2>(acc.c, tile_s + 2 * kPart, fb_hi, fb_lo, lane);
-      pv_mma_quarter<3>(acc.c, tile_s + 3 * kPart, fb_hi, fb_lo, lane);
+      for (int gg = 0; gg < G; ++gg) {
+        const float x = valid ? sc[gg] * nk : -INFINITY;
+        const float m = warp_max(x);
+        const float p = m == -INFINITY ? 0.0f : exp2f(x - m);
+        const float l = warp_sum(p);
+        store_weight(wh, gg, lane, valid ? p * nv : 0.0f);
+        if (lane == 0) ml[grp * G + gg] = make_float2(m, l);
+      }
+      __syncwarp();
+      asm volatile("bar.arrive %0, 64;\n" ::"r"(1 + grp) : "memory");
     } else {
-      pv_mma_half<0>(acc.c, tile_s, fb_hi, fb_lo, lane);
-      pv_mma_half<1>(acc.c, tile_s + kPart, fb_hi, fb_lo, lane);
+      const uint32_t tile_s = static_cast<uint32_t>(__cvta_generic_to_shared(gsm + L.tile));
+      const LevelPool pool_hi = level_pool(a.tabs->v.level16, 0), pool_lo = level_pool(a.tabs->v.level16, 16);
+      constexpr int kCoords = kLo ? kHalf / 2 : kHalf;
+#pragma unroll 1
+      for (int i8 = 0; i8 < kD; i8 += 8) {
+        uint32_t e[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) e[u] = rans_step<kTwo>(rl, lut_v, smem);
+        const uint32_t part = tile_s + (i8 / kCoords) * (kTile * kTileRow);
+        const int chunk = (i8 % kCoords) >> 3;
+        store_levels<kLo>(part + tile_off(lane, chunk), part + tile_off(lane, 4 + chunk), e, pool_hi, pool_lo);
+      }
+      float c[kD / 16][4];
+#pragma unroll
+      for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[mt][k] = 0.0f;
+      asm volatile("bar.sync %0, 64;\n" ::"r"(1 + grp) : "memory");
+      uint32_t fb_hi[2][2], fb_lo[2][2];
+      load_weights<G>(wh, fb_hi, fb_lo, lane);
+      constexpr int kPart = kTile * kTileRow;
+      if constexpr (kLo) {
+        pv_mma_quarter<0>(c, tile_s, fb_hi, fb_lo, lane);
+        pv_mma_quarter<1>(c, tile_s + kPart, fb_hi, fb_lo, lane);
+        pv_mma_quarter<2>(c, tile_s + 2 * kPart, fb_hi, fb_lo, lane);
+        pv_mma_quarter<3>(c, tile_s + 3 * kPart, fb_hi, fb_lo, lane);
+      } else {
+        pv_mma_half<0>(c, tile_s, fb_hi, fb_lo, lane);
+        pv_mma_half<1>(c, tile_s + kPart, fb_hi, fb_lo, lane);
+      }
+      __syncwarp();  // the tile has been read: o takes its place
+      float *o = reinterpret_cast<float *>(gsm + L.tile);
+      const int row = lane >> 2, head0 = 2 * (lane & 3);
+#pragma unroll
+      for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (head0 + (k & 1) < G) o[(head0 + (k & 1)) * kD + 16 * mt + row + 8 * (k >> 1)] = c[mt][k];
     }
-    __syncwarp();  // the tile has been read: o takes its place
-    float *o = reinterpret_cast<float *>(wsm + L.tile);
-    const int row = lane >> 2, head0 = 2 * (lane & 3);
-#pragma unroll
-    for (int mt = 0; mt < kD / 16; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (head0 + (e & 1) < G) o[(head0 + (e & 1)) * kD + 16 * mt + row + 8 * (e >> 1)] = acc.c[mt][e];
-    if (lane == 0)
-#pragma unroll
-      for (int gg = 0; gg < G; ++gg) ml[warp * G + gg] = make_float2(acc.m[gg], acc.l[gg]);
-  } else if (lane < G) {
-    ml[warp * G + lane] = make_float2(-INFINITY, 0.0f);
+    bad_count = __popc(__ballot_sync(kFull, valid && (rl.x != kL || (cb[kTile] & 0x7C) == 0x7C)));
+#ifdef DQ_CHECKED
+    over_count = __popc(__ballot_sync(kFull, valid && overread(rl, cb, smem, is_v ? a.cv : a.ck)));
+#endif
+  } else if (!is_v && lane < G) {
+    ml[grp * G + lane] = make_float2(-INFINITY, 0.0f);
   }
   __syncthreads();
+  cl.barrier_wait();
 
-  // D7 in the CTA: a warp with no group (or no visible token) weighs nothing.
+  // D7 in the CTA, into the owner of each head (head gg belongs to CTA gg %
+  // C): a group with no visible token weighs nothing.
   for (int i = threadIdx.x; i < G * kD; i += blockDim.x) {
     const int gg = i / kD;
     float M = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int w = 0; w < nwarps; ++w) M = fmaxf(M, ml[w * G + gg].x);
+    for (int w = 0; w < groups; ++w) M = fmaxf(M, ml[w * G + gg].x);
     if (M != -INFINITY)
-      for (int w = 0; w < nwarps; ++w) {
+      for (int w = 0; w < groups; ++w) {
         const float2 s = ml[w * G + gg];
         if (s.x == -INFINITY) continue;
         const float r = exp2f(s.x - M);
         l = fmaf(r, s.y, l);
-        o = fmaf(r, reinterpret_cast<const float *>(smem + L.warp0 + w * L.warp_bytes + L.tile)[i], o);
+        o = fmaf(r, reinterpret_cast<const float *>(smem + L.group0 + w * L.group_bytes + L.tile)[i], o);
       }
-    cta_o[i] = o;
-    if (i % kD == 0) cta_ml[gg] = make_float2(M, l);
+    const int slot = (gg / C) * C + rank;
+    cl.map_shared_rank(own_o, gg % C)[slot * kD + i % kD] = o;
+    if (i % kD == 0) cl.map_shared_rank(own_ml, gg % C)[slot] = make_float2(M, l);
   }
   cl.sync();
 
-  // D7 in the cluster: head gg belongs to CTA gg % C.
-  for (int gg = rank + C * warp; gg < G; gg += C * nwarps) {
-    const float2 s = lane < C ? cl.map_shared_rank(cta_ml, lane)[gg] : make_float2(-INFINITY, 0.0f);
+  // D7 of the owned heads.
+  for (int k0 = warp; rank + C * k0 < G; k0 += 2 * groups) {
+    const int gg = rank + C * k0;
+    const float2 s = lane < C ? own_ml[k0 * C + lane] : make_float2(-INFINITY, 0.0f);
     const float M = warp_max(s.x);
     const float r = M == -INFINITY ? 0.0f : exp2f(s.x - M);
     const float l = warp_sum(r * s.y);
@@ -1045,9 +1088,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
 #pragma unroll 4
     for (int c = 0; c < C; ++c) {
       const float rc = __shfl_sync(kFull, r, c);
-      const float *src = cl.map_shared_rank(cta_o, c) + gg * kD + lane;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = fmaf(rc, src[32 * k], o[k]);
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(rc, own_o[(k0 * C + c) * kD + lane + 32 * k], o[k]);
     }
     const float inv = l > 0.0f ? 1.0f / (l * static_cast<float>(kD) * a.tabs->v.tile_scale) : 0.0f;
     wht128_warp(o, lane);
@@ -1060,9 +1102,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) decode_few_kernel(const Dec
     if (bad_count) atomicAdd(&a.stats->integrity_errors, static_cast<unsigned long long>(bad_count));
     if (bad_pages) atomicAdd(&a.stats->bad_pages, static_cast<unsigned long long>(bad_pages));
     if (over_count) atomicAdd(&a.stats->overreads, static_cast<unsigned long long>(over_count));
+    if (warp == 0 && !ready) atomicAdd(&a.stats->wait_timeouts, 1ull);
     if (warp == 0 && rank == 0 && h == 0 && raw != len) atomicAdd(&a.stats->clamped_lengths, 1ull);
   }
-  cl.sync();  // the other CTAs have read this one's state
 }
 
 int warps_for(int G, int ck, int cv) {
@@ -1133,38 +1175,39 @@ int launch_combine(const DecodeArgs &a, unsigned rows, cudaStream_t st) {
 }
 
 // Launch shape of decode_few_kernel, cluster 0 where it does not serve: the
-// most CTAs per (b, KV head) that the SMs hold at once, and a warp per group.
+// most CTAs per (b, KV head) that the SMs hold at once, and two warps per group.
 struct FewShape {
-  int cluster, warps;
+  int cluster, groups;
 };
 
 FewShape few_shape(const DecodeArgs &a) {
   FewShape s{0, 0};
   const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap, all = (cap + kTile - 1) / kTile;
   const int64_t seen = (a.sinks + kTile - 1) / kTile + (a.window + kTile - 2) / kTile + 1;
-  const int64_t groups = seen < all ? seen : all;  // at most, of one (b, h)
+  const int64_t most = seen < all ? seen : all;  // groups of one (b, h)
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
   if (a.window == 0 || rows > a.grid) return s;
   int C = kFewCluster;
-  while (C > 1 && (rows * C > a.grid || C / 2 >= groups)) C /= 2;
-  const int64_t nw = groups > C ? (groups + C - 1) / C : 1;
-  if (nw > kFewWarps || few_smem_layout(a.G, a.ck, a.cv, a.out_dtype == DQ_F32, static_cast<int>(nw)).total > 227 * 1024)
+  while (C > 1 && (rows * C > a.grid || C / 2 >= most)) C /= 2;
+  const int64_t n = most > C ? (most + C - 1) / C : 1;
+  if (n > kFewGroups ||
+      few_smem_layout(a.G, a.ck, a.cv, a.out_dtype == DQ_F32, static_cast<int>(n), C).total > 227 * 1024)
     return s;
   s.cluster = C;
-  s.warps = static_cast<int>(nw);
+  s.groups = static_cast<int>(n);
   return s;
 }
 
 template <int G, bool kTwo, bool kLo>
 int launch_few(const DecodeArgs &a, FewShape f, cudaStream_t st) {
-  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, f.warps);
+  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, f.groups, f.cluster);
   constexpr auto kern = decode_few_kernel<G, kTwo, kLo>;
   cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
   if (e == cudaSuccess) e = allow_wide_cluster<kern>();
   if (e != cudaSuccess) return static_cast<int>(e);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hkv * f.cluster));
-  cfg.blockDim = dim3(static_cast<unsigned>(f.warps * 32));
+  cfg.blockDim = dim3(static_cast<unsigned>(f.groups * 64));
   cfg.dynamicSmemBytes = L.total;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
