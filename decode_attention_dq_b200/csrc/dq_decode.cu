@@ -1174,59 +1174,84 @@ int launch_combine(const DecodeArgs &a, unsigned rows, cudaStream_t st) {
   return static_cast<int>(cudaGetLastError());
 }
 
-// Launch shape of decode_few_kernel, cluster 0 where it does not serve: the
-// most CTAs per (b, KV head) that the SMs hold at once, and two warps per group.
-struct FewShape {
-  int cluster, groups;
-};
-
-FewShape few_shape(const DecodeArgs &a) {
-  FewShape s{0, 0};
-  const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap, all = (cap + kTile - 1) / kTile;
-  const int64_t seen = (a.sinks + kTile - 1) / kTile + (a.window + kTile - 2) / kTile + 1;
-  const int64_t most = seen < all ? seen : all;  // groups of one (b, h)
-  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
-  if (a.window == 0 || rows > a.grid) return s;
-  int C = kFewCluster;
-  while (C > 1 && (rows * C > a.grid || C / 2 >= most)) C /= 2;
-  const int64_t n = most > C ? (most + C - 1) / C : 1;
-  if (n > kFewGroups ||
-      few_smem_layout(a.G, a.ck, a.cv, a.out_dtype == DQ_F32, static_cast<int>(n), C).total > 227 * 1024)
-    return s;
-  s.cluster = C;
-  s.groups = static_cast<int>(n);
-  return s;
-}
-
-template <int G, bool kTwo, bool kLo>
-int launch_few(const DecodeArgs &a, FewShape f, cudaStream_t st) {
-  const FewSmem L = few_smem_layout(G, a.ck, a.cv, kLo, f.groups, f.cluster);
-  constexpr auto kern = decode_few_kernel<G, kTwo, kLo>;
-  cudaError_t e = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
-  if (e == cudaSuccess) e = allow_wide_cluster<kern>();
-  if (e != cudaSuccess) return static_cast<int>(e);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hkv * f.cluster));
-  cfg.blockDim = dim3(static_cast<unsigned>(f.groups * 64));
-  cfg.dynamicSmemBytes = L.total;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
+// Launch of `rows` clusters of C CTAs with n groups each.
+void few_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, int C, int n, size_t smem, int rows) {
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
+  cfg.blockDim = dim3(static_cast<unsigned>(n * 64));
+  cfg.dynamicSmemBytes = smem;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(f.cluster);
+  attr.val.clusterDim.x = static_cast<unsigned>(C);
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+// Clusters of C CTAs with n groups each that the device holds at once (what
+// cudaOccupancyMaxActiveClusters says; asked again only for another shared
+// memory size; 0: none). The SMs' groups are uneven, so it is less than SMs / C.
+template <auto Kern>
+int few_capacity(int C, int n, size_t smem) {
+  constexpr int kDevs = 64;
+  static std::atomic<uint64_t> known[kDevs][5][kFewGroups + 1];  // smem << 16 | capacity
+  if (smem > 227 * 1024) return 0;
+  int dev = 0, c = 0;
+  while ((1 << c) < C) ++c;
+  if (cudaGetDevice(&dev) != cudaSuccess || ensure_max_dynamic_smem<Kern>(static_cast<int>(smem)) != cudaSuccess ||
+      allow_wide_cluster<Kern>() != cudaSuccess)
+    return 0;
+  const bool cached = dev >= 0 && dev < kDevs;
+  if (cached) {
+    const uint64_t k = known[dev][c][n].load(std::memory_order_acquire);
+    if (k >> 16 == smem) return static_cast<int>(k & 0xFFFF);
+  }
+  int clusters = 0;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  few_config(cfg, attr, C, n, smem, 1);
+  if (cudaOccupancyMaxActiveClusters(&clusters, Kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // (not held against the launch that follows)
+    clusters = 0;
+  }
+  if (cached) known[dev][c][n].store(static_cast<uint64_t>(smem) << 16 | static_cast<unsigned>(clusters), std::memory_order_release);
+  return clusters;
+}
+
+// Launches decode_few_kernel where it serves: the largest cluster with a pair
+// of warps for every group of a (b, h) and room for all (b, h) at once.
+// Returns -1 where there is none. (Against the balanced split: 14.4 and 25.7
+// us for 8 rows of 34 groups, 17.6 and 28.0 us for 32; in two rounds of
+// clusters it is the slower one, 28.6 and 25.0 us for 16 rows of 65.)
+template <int G, bool kTwo, bool kLo>
+int launch_few(const DecodeArgs &a, cudaStream_t st) {
+  constexpr auto kern = decode_few_kernel<G, kTwo, kLo>;
+  const int64_t cap = a.T_max < a.T_cap ? a.T_max : a.T_cap, all = (cap + kTile - 1) / kTile;
+  const int64_t seen = (a.sinks + kTile - 1) / kTile + (a.window + kTile - 2) / kTile + 1;
+  const int64_t most = seen < all ? (seen > 0 ? seen : 1) : (all > 0 ? all : 1);  // groups of one (b, h)
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv;
+  if (rows > a.grid || most > kFewGroups * kFewCluster) return -1;
+  for (int C = kFewCluster; C >= 1; C /= 2) {
+    const int n = static_cast<int>((most + C - 1) / C);
+    if (C > 1 && C / 2 >= most) continue;
+    if (n > kFewGroups) return -1;
+    const size_t smem = few_smem_layout(G, a.ck, a.cv, kLo, n, C).total;
+    if (rows > few_capacity<kern>(C, n, smem)) continue;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    few_config(cfg, attr, C, n, smem, static_cast<int>(rows));
+    cfg.stream = st;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kern, a));
+  }
+  return -1;
 }
 
 template <bool kTwo, bool kLo>
-int launch_few_g(const DecodeArgs &a, FewShape f, cudaStream_t st) {
+int launch_few_g(const DecodeArgs &a, cudaStream_t st) {
   switch (a.G) {
-    case 1: return launch_few<1, kTwo, kLo>(a, f, st);
-    case 2: return launch_few<2, kTwo, kLo>(a, f, st);
-    case 4: return launch_few<4, kTwo, kLo>(a, f, st);
-    case 8: return launch_few<8, kTwo, kLo>(a, f, st);
+    case 1: return launch_few<1, kTwo, kLo>(a, st);
+    case 2: return launch_few<2, kTwo, kLo>(a, st);
+    case 4: return launch_few<4, kTwo, kLo>(a, st);
+    case 8: return launch_few<8, kTwo, kLo>(a, st);
     default: return static_cast<int>(cudaErrorInvalidValue);
   }
 }
@@ -1242,10 +1267,11 @@ int decode_warps_per_cta(int G, int ck, int cv) {
 int launch_decode_attention(const DecodeArgs &a, void *stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.ck > kMaxContainer || a.cv > kMaxContainer || a.grid < 1) return static_cast<int>(cudaErrorInvalidValue);
-  if (const FewShape f = few_shape(a); f.cluster > 0) {
+  if (a.window > 0) {
     const bool two = a.two_k || a.two_v, lo = a.out_dtype == DQ_F32;
-    if (two) return lo ? launch_few_g<true, true>(a, f, st) : launch_few_g<true, false>(a, f, st);
-    return lo ? launch_few_g<false, true>(a, f, st) : launch_few_g<false, false>(a, f, st);
+    const int few = two ? (lo ? launch_few_g<true, true>(a, st) : launch_few_g<true, false>(a, st))
+                        : (lo ? launch_few_g<false, true>(a, st) : launch_few_g<false, false>(a, st));
+    if (few >= 0) return few;
   }
   const int e = a.window == 0 ? launch_groups<false, false>(a, st)
                 : a.out_dtype == DQ_F32 ? launch_groups<true, true>(a, st)
