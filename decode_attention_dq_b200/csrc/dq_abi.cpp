@@ -769,7 +769,7 @@ int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_ref
     a.lens_out = d_lens_out;
     a.window = std::min<int64_t>(window, int64_t(1) << 40);  // (any length is below)
     a.sinks = std::min<int64_t>(sinks, int64_t(1) << 40);
-    const int e = dqi::launch_pages_advance(a, stream);
+    const int e = dqi::launch_pages_advance(a, t->sm_count, stream);
     return e == 0 ? DQ_OK : cuda_fail(static_cast<cudaError_t>(e));
   } catch (...) {
     return DQ_ERR_CUDA;

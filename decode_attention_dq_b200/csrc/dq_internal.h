@@ -192,7 +192,7 @@ struct PagesLayout {
   size_t list, need, lo, hi, map, movers, total;
 };
 PagesLayout pages_layout(int64_t num_pages, int64_t B, int64_t max_pages);
-int launch_pages_advance(const PagesArgs &a, void *stream);
+int launch_pages_advance(const PagesArgs &a, int sm_count, void *stream);
 int launch_pages_fork(const PagesArgs &a, void *stream);
 int launch_pages_compact(const PagesArgs &a, void *stream);
 

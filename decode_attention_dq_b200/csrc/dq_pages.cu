@@ -234,65 +234,118 @@ __device__ __forceinline__ void copy_refs(const PagesArgs &a, long long lo, long
   for_quads(a.refs_in, lo, hi, vec, 0, [&](long long p, const int (&v)[4]) { store4(a.refs_out, p, hi, vec, v); });
 }
 
+struct RowCounts {
+  int released, bad, clamped;
+};
+
+// One work item of dq_pages_advance, by a warp: what is given back, and how
+// many entries want a page.
+__device__ __forceinline__ void advance_item(const PagesArgs &a, long long it, long long nseg, long long cap, bool vec,
+                                             RowCounts &n_of) {
+  const int lane = threadIdx.x & 31;
+  const long long P = a.num_pages, mp = a.max_pages;
+  const long long b = it / nseg, j0 = (it % nseg) * kSeg, j1 = j0 + kSeg < mp ? j0 + kSeg : mp;
+  const int raw = a.lens_in[b], n = a.step[b];
+  const long long len = clamp_tokens(raw, cap), want = n < 0 ? 0 : len + n;
+  const long long len2 = want < cap ? want : cap;
+  if (j0 == 0 && lane == 0) n_of.clamped += (raw != len || want != len2) ? 1 : 0;
+  // Blocks [g_lo, g_hi) are given back; blocks [t_lo, t_hi) need a page.
+  long long g_lo = 0, g_hi = n < 0 ? mp : 0;
+  if (n >= 0 && a.window > 0) {
+    g_lo = (a.sinks + kPage - 1) / kPage;
+    const long long seen = len + 1 - a.window;  // the first token that a next one sees
+    g_hi = seen > 0 ? seen / kPage : 0;
+  }
+  const long long t_lo = n < 0 ? 0 : len / kPage, t_hi = n < 0 ? 0 : (len2 + kPage - 1) / kPage;
+  int32_t *out = a.table_out + b * mp;
+  int need = 0;
+  for_quads(a.table_in + b * mp, j0, j1, vec, -1, [&](long long j, const int (&e)[4]) {
+    int v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool held = e[k] >= 0 && e[k] < P;
+      const bool gone = j + k >= g_lo && j + k < g_hi;
+      n_of.bad += (!held && e[k] != -1) ? 1 : 0;
+      if (held && gone) {
+        atomicSub(a.refs_out + e[k], 1);
+        ++n_of.released;
+      }
+      v[k] = held && !gone ? e[k] : -1;
+      need += (v[k] < 0 && j + k >= t_lo && j + k < t_hi) ? 1 : 0;
+    }
+    store4(out, j, j1, vec, v);
+  });
+  need = __reduce_add_sync(kFull, need);
+  if (lane == 0) {
+    a.item_need[it] = need;
+    a.item_lo[it] = static_cast<int32_t>(t_lo > j0 ? t_lo : j0);
+    a.item_hi[it] = static_cast<int32_t>(t_hi < j1 ? t_hi : j1);
+  }
+}
+
+__device__ __forceinline__ long long max_tokens(const PagesArgs &a) {
+  return kPage * a.max_pages < 0x7FFFFFFF ? kPage * a.max_pages : 0x7FFFFFFF;
+}
+__device__ __forceinline__ bool aligned_rows(const PagesArgs &a) {
+  return aligned16(a.table_in) && aligned16(a.table_out) && a.max_pages % 4 == 0;
+}
+
+// Large states: the counts' copy and the rows on all SMs, in two launches of
+// their own before advance_kernel<false>; the rows' counts gather in d_counts.
+__global__ void __launch_bounds__(kThreads) advance_copy_kernel(const PagesArgs a) {
+  const long long warps = static_cast<long long>(gridDim.x) * kWarps;
+  if (blockIdx.x == 0 && threadIdx.x < 8) a.counts[threadIdx.x] = 0;
+  if (a.refs_out == a.refs_in) return;
+  long long lo, hi;
+  part((a.num_pages + 3) / 4, static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5), warps, lo, hi);
+  hi = hi * 4 < a.num_pages ? hi * 4 : a.num_pages;
+  copy_refs(a, lo * 4, hi, aligned16(a.refs_in) && aligned16(a.refs_out));
+}
+__global__ void __launch_bounds__(kThreads) advance_rows_kernel(const PagesArgs a) {
+  const long long nseg = (a.max_pages + kSeg - 1) / kSeg, items = a.B_in * nseg;
+  RowCounts n{0, 0, 0};
+  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
+       it += static_cast<long long>(gridDim.x) * kWarps)
+    advance_item(a, it, nseg, max_tokens(a), aligned_rows(a), n);
+  n.released = __reduce_add_sync(kFull, n.released);
+  n.bad = __reduce_add_sync(kFull, n.bad);
+  n.clamped = __reduce_add_sync(kFull, n.clamped);
+  if ((threadIdx.x & 31) == 0) {
+    if (n.released) atomicAdd(a.counts + 2, n.released);
+    if (n.bad) atomicAdd(a.counts + 4, n.bad);
+    if (n.clamped) atomicAdd(a.counts + 5, n.clamped);
+  }
+}
+
+// kRows: with the copy of the counts and the rows; else they have been done.
+template <bool kRows>
 __global__ void __launch_bounds__(kThreads, 1) advance_kernel(const PagesArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   __shared__ Shared sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(cl.block_rank());
-  const long long P = a.num_pages, mp = a.max_pages, cap = kPage * mp < 0x7FFFFFFF ? kPage * mp : 0x7FFFFFFF;
+  const long long P = a.num_pages, mp = a.max_pages, cap = max_tokens(a);
   const long long nseg = (mp + kSeg - 1) / kSeg, items = a.B_in * nseg;
   const bool vec_refs = aligned16(a.refs_in) && aligned16(a.refs_out);
-  const bool vec_rows = aligned16(a.table_in) && aligned16(a.table_out) && mp % 4 == 0;
   if (threadIdx.x == 0) sh.totals = Totals{};
   long long w_lo, w_hi, i_lo, i_hi;
   warp_part(P, rank, w_lo, w_hi);
   part(items, rank, kCluster, i_lo, i_hi);
-  if (a.refs_out != a.refs_in) copy_refs(a, w_lo, w_hi, vec_refs);
-  cl.sync();
-
-  // Rows: what is given back, and how many entries of each item want a page.
-  int released = 0, bad = 0, clamped = 0;
-  for (long long it = i_lo + warp; it < i_hi; it += kWarps) {
-    const long long b = it / nseg, j0 = (it % nseg) * kSeg, j1 = j0 + kSeg < mp ? j0 + kSeg : mp;
-    const int raw = a.lens_in[b], n = a.step[b];
-    const long long len = clamp_tokens(raw, cap), want = n < 0 ? 0 : len + n;
-    const long long len2 = want < cap ? want : cap;
-    if (j0 == 0 && lane == 0) clamped += (raw != len || want != len2) ? 1 : 0;
-    // Blocks [g_lo, g_hi) are given back; blocks [t_lo, t_hi) need a page.
-    long long g_lo = 0, g_hi = n < 0 ? mp : 0;
-    if (n >= 0 && a.window > 0) {
-      g_lo = (a.sinks + kPage - 1) / kPage;
-      const long long seen = len + 1 - a.window;  // the first token that a next one sees
-      g_hi = seen > 0 ? seen / kPage : 0;
-    }
-    const long long t_lo = n < 0 ? 0 : len / kPage, t_hi = n < 0 ? 0 : (len2 + kPage - 1) / kPage;
-    int32_t *out = a.table_out + b * mp;
-    int need = 0;
-    for_quads(a.table_in + b * mp, j0, j1, vec_rows, -1, [&](long long j, const int (&e)[4]) {
-      int v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool held = e[k] >= 0 && e[k] < P;
-        const bool gone = j + k >= g_lo && j + k < g_hi;
-        bad += (!held && e[k] != -1) ? 1 : 0;
-        if (held && gone) {
-          atomicSub(a.refs_out + e[k], 1);
-          ++released;
-        }
-        v[k] = held && !gone ? e[k] : -1;
-        need += (v[k] < 0 && j + k >= t_lo && j + k < t_hi) ? 1 : 0;
-      }
-      store4(out, j, j1, vec_rows, v);
-    });
-    need = __reduce_add_sync(kFull, need);
-    if (lane == 0) {
-      a.item_need[it] = need;
-      a.item_lo[it] = static_cast<int32_t>(t_lo > j0 ? t_lo : j0);
-      a.item_hi[it] = static_cast<int32_t>(t_hi < j1 ? t_hi : j1);
+  if constexpr (kRows) {
+    if (a.refs_out != a.refs_in) copy_refs(a, w_lo, w_hi, vec_refs);
+    cl.sync();
+    RowCounts n{0, 0, 0};
+    for (long long it = i_lo + warp; it < i_hi; it += kWarps) advance_item(a, it, nseg, cap, aligned_rows(a), n);
+    add_counts(&sh.totals, n.released, n.bad, n.clamped, 0);
+    cl.sync();
+  } else {
+    __syncthreads();
+    if (rank == 0 && threadIdx.x == 0) {
+      sh.totals.released = a.counts[2];
+      sh.totals.bad = a.counts[4];
+      sh.totals.clamped = a.counts[5];
     }
   }
-  add_counts(&sh.totals, released, bad, clamped, 0);
-  cl.sync();
 
   // Lengths (all have been read); needs of this CTA; free pages of its part.
   for (long long b = static_cast<long long>(rank) * kThreads + threadIdx.x; b < a.B_in; b += kCluster * kThreads) {
@@ -316,27 +369,25 @@ __global__ void __launch_bounds__(kThreads, 1) advance_kernel(const PagesArgs a)
   list_free(a.refs_out, w_lo, w_hi, vec_refs, before.free_pages + w_before, take, a.list, a.refs_out);
   cl.sync();
 
-  // The items' entries, in their order.
+  // The items' entries, in their order: the rank of each item's first one,
+  // then an item per warp.
+  __shared__ long long first[kThreads];
   long long base = before.need;
   for (long long c0 = i_lo; c0 < i_hi; c0 += kThreads) {
-    // Rank of the first entry of each of the next kThreads items.
     const long long it = c0 + threadIdx.x;
-    const int n = it < i_hi ? a.item_need[it] : 0;
     int in_warp;
-    const int before_lane = lane_exclusive(n, in_warp);
-    const long long first = base + block_exclusive(in_warp, sh.scan, total) + before_lane;
+    const int before_lane = lane_exclusive(it < i_hi ? a.item_need[it] : 0, in_warp);
+    first[threadIdx.x] = base + block_exclusive(in_warp, sh.scan, total) + before_lane;
     base += total;
-    // The warp serves its own 32 items.
-    unsigned todo = __ballot_sync(kFull, n > 0);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const long long id = c0 + warp * 32 + src;
-      long long r = __shfl_sync(kFull, first, src);
+    __syncthreads();
+    for (long long id = c0 + warp; id < i_hi && id < c0 + kThreads; id += kWarps) {
+      if (a.item_need[id] == 0) continue;
+      long long r = first[id - c0];
       int32_t *out = a.table_out + (id / nseg) * mp;
-      for (int j0 = a.item_lo[id]; j0 < a.item_hi[id]; j0 += 32) {
+      const int hi = a.item_hi[id];
+      for (int j0 = a.item_lo[id]; j0 < hi; j0 += 32) {
         const int j = j0 + lane;
-        const bool w = j < a.item_hi[id] && __ldcg(out + j) < 0;
+        const bool w = j < hi && __ldcg(out + j) < 0;
         const unsigned m = __ballot_sync(kFull, w);
         if (w) {
           const long long x = r + ballot_rank(m);
@@ -345,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) advance_kernel(const PagesArgs a)
         r += __popc(m);
       }
     }
+    __syncthreads();  // `first` is written again
   }
 }
 
@@ -640,6 +692,11 @@ int launch_cluster(const PagesArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+// Counts and table entries up to which dq_pages_advance is one launch. (One
+// launch and three: 12.8 and 15.1 us for 41 thousand, 17.5 and 18.4 us for 462
+// thousand, 25.9 and 22.0 us for 924 thousand, 37.6 and 25.0 us for 1.6 million.)
+constexpr int64_t kOneLaunch = int64_t(5) << 17;
+
 PagesLayout pages_layout(int64_t num_pages, int64_t B, int64_t max_pages) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   PagesLayout l;
@@ -655,8 +712,16 @@ PagesLayout pages_layout(int64_t num_pages, int64_t B, int64_t max_pages) {
   return l;
 }
 
-int launch_pages_advance(const PagesArgs &a, void *stream) {
-  return launch_cluster<advance_kernel>(a, static_cast<cudaStream_t>(stream));
+int launch_pages_advance(const PagesArgs &a, int sm_count, void *stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.num_pages + a.B_in * a.max_pages <= kOneLaunch) return launch_cluster<advance_kernel<true>>(a, st);
+  advance_copy_kernel<<<sm_count, kThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  advance_rows_kernel<<<sm_count, kThreads, 0, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return static_cast<int>(e);
+  return launch_cluster<advance_kernel<false>>(a, st);
 }
 int launch_pages_fork(const PagesArgs &a, void *stream) {
   return launch_cluster<fork_kernel>(a, static_cast<cudaStream_t>(stream));

@@ -61,6 +61,20 @@ def test_advance(tab, P, B, mp, in_place):
               "window %d sinks %d" % (window, sinks))
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_advance_of_a_large_state(tab, in_place):
+    # More counts and entries than one launch takes: the rows go on all SMs.
+    rng = np.random.default_rng(5)
+    P, B, mp = 660001, 30, 701
+    for window, sinks in ((0, 0), (900, 40)):
+        refs, table, lens = R.random_state(rng, P, B, mp, window=window, sinks=sinks)
+        table[3, 5], table[4, 6], lens[7] = P, -9, -50
+        refs[:200000] = 1
+        n = rng.choice([-1, 0, 1, 33, 200, 9000], B)
+        _same(_advance(tab, refs, table, lens, n, window, sinks, in_place), R.advance(refs, table, lens, n, window, sinks),
+              "window %d sinks %d" % (window, sinks))
+
+
 def test_advance_hands_out_what_it_takes_back(tab):
     # A full pool: rows 0 and 2 end, row 1 grows into their pages.
     table = np.array([[5, 4, -1, -1], [1, -1, -1, -1], [0, 2, 3, -1]])
