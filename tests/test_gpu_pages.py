@@ -84,6 +84,44 @@ def test_advance_hands_out_what_it_takes_back(tab):
                 dict(free_pages=2, taken=3, released=5, short_of=0, bad=0, clamped=0, pairs=0, reserved=0)), "full pool")
 
 
+def test_many_short_rows(tab):
+    # More rows than a CTA's part is wide.
+    rng = np.random.default_rng(2)
+    P, B, mp = 30000, 18000, 2
+    refs, table, lens = R.random_state(rng, P, B, mp)
+    n = rng.choice([-1, 0, 1, 1, 40], B)
+    _same(_advance(tab, refs, table, lens, n), R.advance(refs, table, lens, n), "advance")
+    parent = rng.integers(-1, B, 20000)
+    _same(_fork(tab, refs, table, lens, parent), R.fork(refs, table, lens, parent), "fork")
+    _same(_compact(tab, refs, table), R.compact(refs, table), "compact")
+
+
+def test_arrays_that_start_anywhere(tab):
+    # Four-byte aligned views: no 16-byte accesses.
+    rng = np.random.default_rng(3)
+    P, B, mp = 5000, 12, 64
+
+    def off(x):
+        x = _ints(x)
+        buf = torch.full((x.numel() + 1,), -77, dtype=torch.int32, device="cuda")
+        buf[1:] = x.reshape(-1)
+        return buf[1:].view(x.shape)
+
+    refs, table, lens = R.random_state(rng, P, B, mp)
+    n, ws, c = rng.choice([-1, 1, 90], B), _workspace(tab, P, B, mp), dq.new_page_counts()
+    o = [off(np.full_like(x, -77)) for x in (refs, table, lens)]
+    dq.dq_pages_advance(tab, off(refs), off(table), off(lens), off(n), *o, c, ws)
+    _same((*o, c), R.advance(refs, table, lens, n), "advance")
+    pairs = off(np.zeros((B, 2)))
+    parent = rng.integers(-1, B, B)
+    o = [off(np.full_like(x, -77)) for x in (refs, table, lens)]
+    dq.dq_pages_fork(tab, off(refs), off(table), off(lens), off(parent), *o, pairs, c, ws)
+    _same((*o, pairs, c), R.fork(refs, table, lens, parent), "fork")
+    o, pairs = [off(np.full_like(x, -77)) for x in (refs, table)], off(np.zeros((P // 2, 2)))
+    dq.dq_pages_compact(tab, off(refs), off(table), *o, pairs, c, ws)
+    _same((*o, pairs, c), R.compact(refs, table), "compact")
+
+
 def test_advance_out_of_range(tab):
     # Lengths beyond the table and negative ones, entries that are no pages, a pool too small.
     table = np.array([[0, 99, -7], [1, 2, 3], [2 ** 31 - 1, -1, 4], [-2 ** 31, -1, -1]])

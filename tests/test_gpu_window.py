@@ -330,6 +330,27 @@ def test_prefill_in_waves_is_bit_identical():
         _prefill(lib, q, kc, vc, start, window, sinks, workspace=torch.empty(row - 16, dtype=torch.uint8, device="cuda"))
 
 
+def test_offsets_past_four_gigabytes():
+    # 2^27 tokens, 4.8 GB per stream: the first 5 and the last 100 are there, the rest is garbage.
+    B, Hkv, G, T, far = 1, 1, 4, 105, 2 ** 27
+    w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T)
+    K, V, _ = cm.inputs(w)
+    big = [torch.full((1, 1, far, 36), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for part, at in ((slice(0, 5), 0), (slice(5, 105), far - 100)):
+        k, v = (torch.from_numpy(x[:, :, part]).cuda().bfloat16().contiguous() for x in (K, V))
+        dq.dq_append_kv(lib, k, v, _ints([at]), *big)
+    q = synth.q_block(w)
+    want, bound = W.attention(ref, q[:, None], rk, rv, [T - 1], T, 0, chunk=False, half_levels=False)
+    stats = dq.new_stats()
+    W.assert_within(_np(_decode(lib, q, *big, [far], 100, 5, stats=stats)), want[:, 0], bound[:, 0], False, "decode")
+    # The same 60 tokens and first 5 for every query of a chunk, wherever they are.
+    qc = synth.q_chunk(w, 40)
+    want, bound = W.attention(ref, qc, rk, rv, [T - 40], 60, 5, chunk=True)
+    W.assert_within(_np(_prefill(lib, qc, *big, [far - 40], 60, 5, stats=stats)), want, bound, False, "chunk")
+    s = dq.stats_dict(stats)
+    assert s["wait_timeouts"] == 0 and s["clamped_lengths"] == 0 and s["integrity_errors"] == 0
+
+
 def test_tiny_queries_and_scales_stay_finite():
     # Logits far below one step: the weights are equal, masked tokens weigh nothing.
     B, Hkv, G, T = 1, 1, 4, 200
