@@ -50,7 +50,7 @@ constexpr int kSeg = 32 * 4 * kQuads;  // table entries that a warp handles at a
 // A CTA's part of the counts that the cluster exchanges.
 struct Totals {
   long long free_pages, need;
-  int released, bad, clamped, gained;  // gained: pages that became free less pages that ceased to be
+  int released, bad, clamped;
 };
 
 struct Shared {
@@ -146,16 +146,14 @@ __device__ __forceinline__ long long clamp_tokens(int len, long long cap) {
 }
 
 // Adds a thread's counts to the CTA's.
-__device__ __forceinline__ void add_counts(Totals *mine, int released, int bad, int clamped, int gained) {
+__device__ __forceinline__ void add_counts(Totals *mine, int released, int bad, int clamped) {
   released = __reduce_add_sync(kFull, released);
   bad = __reduce_add_sync(kFull, bad);
   clamped = __reduce_add_sync(kFull, clamped);
-  gained = __reduce_add_sync(kFull, gained);
   if ((threadIdx.x & 31) == 0) {
     if (released) atomicAdd(&mine->released, released);
     if (bad) atomicAdd(&mine->bad, bad);
     if (clamped) atomicAdd(&mine->clamped, clamped);
-    if (gained) atomicAdd(&mine->gained, gained);
   }
 }
 
@@ -175,7 +173,6 @@ __device__ __forceinline__ void exchange(cg::cluster_group &cl, Shared &sh, Tota
     t.released = __reduce_add_sync(kFull, t.released);
     t.bad = __reduce_add_sync(kFull, t.bad);
     t.clamped = __reduce_add_sync(kFull, t.clamped);
-    t.gained = __reduce_add_sync(kFull, t.gained);
     if (lane == 0) {
       sh.before = b;
       sh.all = t;
@@ -336,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) advance_kernel(const PagesArgs a)
     cl.sync();
     RowCounts n{0, 0, 0};
     for (long long it = i_lo + warp; it < i_hi; it += kWarps) advance_item(a, it, nseg, cap, aligned_rows(a), n);
-    add_counts(&sh.totals, n.released, n.bad, n.clamped, 0);
+    add_counts(&sh.totals, n.released, n.bad, n.clamped);
     cl.sync();
   } else {
     __syncthreads();
@@ -421,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
   copy_refs(a, w_lo, w_hi, vec_refs);
   cl.sync();
 
-  int bad = 0, clamped = 0, gained = 0;
+  int bad = 0, clamped = 0;
   for (long long c = tid; c < a.B_out; c += threads) {
     const int p = a.step[c];
     if (p >= 0 && p < a.B_in) {
@@ -437,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
   // Whether a row's last page t stays with its first child: nobody else may
   // hold it.
   auto stays = [&](int t) { return __ldcg(a.refs_in + t) == 1; };
-  // Items [0, B_in nseg): the old rows' references go, the children's come.
-  // Items from there on: the new rows.
-  const long long old_items = a.B_in * nseg, items = old_items + a.B_out * nseg;
-  for (long long it = static_cast<long long>(rank) * kWarps + warp; it < items; it += kCluster * kWarps) {
-    const bool is_new = it >= old_items;
-    const long long row = (is_new ? it - old_items : it) / nseg, seg = (is_new ? it - old_items : it) % nseg;
+  // The old rows' references go, the children's come (items of all rows, over
+  // the cluster); then the new rows (those whose new pages this CTA hands out,
+  // so that it knows how many they are).
+  int need = 0;
+  auto do_item = [&](bool is_new, long long it) {
+    const long long row = it / nseg, seg = it % nseg;
     const long long j0 = seg * kSeg, j1 = j0 + kSeg < mp ? j0 + kSeg : mp;
     const int parent = is_new ? a.step[row] : static_cast<int>(row);
     const bool real = parent >= 0 && parent < a.B_in;
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
     const long long col = len % kPage ? len / kPage : -1;  // the partly filled block
     if (!is_new && seg == 0 && lane == 0 && raw != len) ++clamped;
     const int kids = real ? __ldcg(a.children + parent) : 0;
-    if (!is_new && kids == 1 && !(col >= j0 && col < j1)) continue;  // its pages keep their references
+    if (!is_new && kids == 1 && !(col >= j0 && col < j1)) return;  // its pages keep their references
     const bool is_first = is_new && real && __ldcg(a.first + parent) == row;
     int32_t *out = a.table_out + row * mp;
     if (!real) {  // a row without a parent (there may be no old table at all)
@@ -460,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
         a.lens_out[row] = 0;
         a.item_need[row] = 0;
       }
-      continue;
+      return;
     }
     for_quads(a.table_in + parent * mp, j0, j1, vec_rows, -1, [&](long long j, const int (&e)[4]) {
       int v[4];
@@ -472,16 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
           bad += (!held && e[k] != -1) ? 1 : 0;
           if (last) {
             const bool copy = held && !(is_first && stays(e[k]));
+            need += copy ? 1 : 0;
             a.item_need[row] = copy ? 1 : 0;
             a.item_lo[row] = v[k];  // the page to copy from
             if (copy) v[k] = -1;
           }
         } else if (held) {
           const int d = last ? (kids > 0 && stays(e[k]) ? 0 : -1) : kids - 1;
-          if (d) {
-            const int was = atomicAdd(a.refs_out + e[k], d);
-            gained += (was + d == 0) - (was == 0);
-          }
+          if (d) atomicAdd(a.refs_out + e[k], d);
         }
       }
       if (is_new) store4(out, j, j1, vec_rows, v);
@@ -490,15 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
       a.lens_out[row] = static_cast<int32_t>(len);
       if (col < 0) a.item_need[row] = 0;
     }
-  }
-  add_counts(&sh.totals, 0, bad, clamped, gained);
+  };
+  for (long long it = static_cast<long long>(rank) * kWarps + warp; it < a.B_in * nseg; it += kCluster * kWarps)
+    do_item(false, it);
+  for (long long it = c_lo * nseg + warp; it < c_hi * nseg; it += kWarps) do_item(true, it);
+  add_counts(&sh.totals, 0, bad, clamped);
   long long total;
   const long long w_before = block_exclusive(mine, sh.scan, total);
   if (threadIdx.x == 0) sh.totals.free_pages = total;
-  cl.sync();
-
-  long long need = 0;
-  for (long long c = c_lo + threadIdx.x; c < c_hi; c += kThreads) need += __ldcg(a.item_need + c);
   block_exclusive(warp_total(need), sh.scan, total);
   if (threadIdx.x == 0) sh.totals.need = total;
   cl.sync();
@@ -506,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
   exchange(cl, sh, before, all);
   const long long take = all.need < all.free_pages ? all.need : all.free_pages;
   if (rank == 0 && threadIdx.x == 0)
-    write_counts(a.counts, all.free_pages + all.gained - take, take, 0, all.need - take, all.bad, all.clamped, take);
+    write_counts(a.counts, 0, take, 0, all.need - take, all.bad, all.clamped, take);  // (the free pages are added below)
   list_free(a.refs_in, w_lo, w_hi, vec_refs, before.free_pages + w_before, take, a.list, a.refs_out);
   for (long long i = take + tid; i < a.B_out; i += threads) {
     a.pairs[2 * i] = -1;
@@ -528,6 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
       a.table_out[c * mp + clamp_tokens(a.lens_in[a.step[c]], cap) / kPage] = page;
     }
   }
+  // (Counted at the end: atomics that return what a page had before would
+  // each be waited for.)
+  const long long left = count_free(a.refs_out, w_lo, w_hi, vec_refs);
+  block_exclusive(left, sh.scan, total);
+  if (threadIdx.x == 0 && total) atomicAdd(a.counts, static_cast<int>(total));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PagesArgs a) {
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PagesArgs a)
     }
     store4(a.table_out, i, e_hi, vec, v);
   });
-  add_counts(&sh.totals, 0, bad, 0, 0);
+  add_counts(&sh.totals, 0, bad, 0);
   cl.sync();
   if (rank == 0) {
     exchange(cl, sh, before, all);
@@ -628,10 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PagesArgs a)
 }
 
 // Pages src -> dst of both pools in every layer. A warp copies pieces of
-// kPiece bytes, four 16-byte loads in flight per lane before the first store,
-// 64 warps per SM: 128 KB in flight, enough for the memory's latency (226 MB
-// of pages in 76 us: 6.0 TB/s read and written, 0.92 of a measured copy).
-constexpr int kPiece = 32 * 16 * 4;
+// kPiece bytes, eight 16-byte loads in flight per lane before the first store
+// (two: 5 % slower, four: 2 %). 226 MB of pages take 73 us: 6.2 TB/s read and
+// written, 0.96 of a measured copy.
+constexpr int kLoads = 8;
+constexpr int kPiece = 32 * 16 * kLoads;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBlocksPerSm = 8;
 
@@ -663,12 +663,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
     const int64_t at = static_cast<int64_t>(is_k ? piece : piece - kp) * kPiece + lane * 16;
     const uint8_t *from = pool + src * bytes + at;
     uint8_t *to = pool + dst * bytes + at;
-    uint4 x[4];
+    uint4 x[kLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kLoads; ++k)
       if (at + 512 * k < bytes) x[k] = __ldcs(reinterpret_cast<const uint4 *>(from + 512 * k));
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kLoads; ++k)
       if (at + 512 * k < bytes) __stcs(reinterpret_cast<uint4 *>(to + 512 * k), x[k]);
   }
   if (a.stats && lane == 0 && bad) atomicAdd(&a.stats->bad_pages, static_cast<unsigned long long>(bad));
