@@ -60,13 +60,19 @@
 // holds these slots only, one behind the other, and each CTA walks the part
 // of them that its own 128 / G query tokens see; the rest of a long cache is
 // neither decoded nor read, whatever the page table says there. A CTA then has
-// few blocks: with a window of 1024 (10 or 11 blocks) about 52 thousand cycles,
-// of which 33 thousand are the blocks, 11 thousand the set-up, the query
+// few blocks: with a window of 1024 (10 or 11 blocks) about 49 thousand cycles,
+// of which 31 thousand are the blocks, 11 thousand the set-up, the query
 // rotation and the first scores, 8 thousand the last P.V, the output rotation
-// and the stores (16 sequences x 512 tokens x 8 KV heads, G = 4: 482 us, 0.17
-// of the measured bf16 peak; window 4096: 0.30). Persistent CTAs that ran
-// ahead into the next query block saved a third of the set-up but spilled in
-// the block loop (96 registers) and were 3 % slower.
+// and the stores. Persistent CTAs that ran ahead into the next query block
+// saved a third of the set-up but spilled in the block loop (96 registers) and
+// were 3 % slower.
+// bf16 outputs of a windowed chunk take the weights W as single fp16 values
+// (kLo false): each is off by at most 2^-11 of itself, 2.8e-4 of the output in
+// the mean against the output's own 1.7e-3, P.V is half as many MMAs and the
+// softmax warps, which set the pace, have less to do per weight (3.1 thousand
+// cycles a block, 3.3 with hi + lo, at a higher clock; 16 sequences x 512 tokens x 8
+// KV heads, G = 4, window 1024: 445 us, 482 with hi + lo; 4 x 2048 tokens, G =
+// 8, window 4096: 926 us, 1070; 0.19 and 0.37 of the measured bf16 peak).
 // Every wait is bounded; a CTA that gives up counts it in wait_timeouts,
 // skips the rest of its work and still frees its tensor memory after its MMAs
 // and copies have drained.
@@ -338,6 +344,12 @@ __device__ __forceinline__ void split_pair_trunc(float2 w, uint32_t &hi, uint32_
   const __half2 l = __floats2half2_rn(lf.x, lf.y);
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// A pair of fp32 values as fp16, packed (first value in the low half).
+__device__ __forceinline__ uint32_t pack_pair(float2 w) {
+  const __half2 h = __floats2half2_rn(w.x, w.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // fp16 hi + lo of a pair of fp32 values, packed (first value in the low half).
@@ -650,7 +662,7 @@ __device__ __forceinline__ void wht_4(float (&z)[4]) {
   z[3] = __fsub_rn(a1, a3);
 }
 
-template <bool kWin>
+template <bool kWin, bool kLo>
 __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int ns = kMaxSlots;  // the host checks a.nslots against it
@@ -934,10 +946,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
               const float2 pp = make_float2(ex2(x.x), ex2(x.y));
               ps2 = __fadd2_rn(ps2, pp);
               const float2 nn = *reinterpret_cast<const float2 *>(nv + t);
-              split_pair_trunc(__fmul2_rn(pp, nn), wh[p], wl[p]);
+              if constexpr (kLo) split_pair_trunc(__fmul2_rn(pp, nn), wh[p], wl[p]);
+              else wh[p] = pack_pair(__fmul2_rn(pp, nn));
             }
             tmem_st8(scol + 8 * c, wh);
-            tmem_st8(scol + 16 + 8 * c, wl);
+            if constexpr (kLo) tmem_st8(scol + 16 + 8 * c, wl);
           }
           psum = ps2.x + ps2.y;
         } else {
@@ -954,10 +967,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
                 p1 = ex2(fmaf(u[t + 1], crow, -mx));
               }
               ps[p & 1] += p0 + p1;
-              split_pair(p0 * nv[t], p1 * nv[t + 1], wh[p], wl[p]);
+              if constexpr (kLo) split_pair(p0 * nv[t], p1 * nv[t + 1], wh[p], wl[p]);
+              else wh[p] = pack_pair(make_float2(p0 * nv[t], p1 * nv[t + 1]));
             }
             tmem_st8(scol + 8 * c, wh);
-            tmem_st8(scol + 16 + 8 * c, wl);
+            if constexpr (kLo) tmem_st8(scol + 16 + 8 * c, wl);
           }
           psum = ps[0] + ps[1];
         }
@@ -1143,7 +1157,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prefill_kernel(const PrefillA
           // its columns 8 (ks % 2) .., lo pairs 16 columns further.
           const uint32_t wc = wb + 32 * static_cast<uint32_t>(ks >> 1) + (ks & 1) * 8;
           mma_ts(tbase + kColO, wc, bd, idO, (jj > 0 || ks > 0) ? 1u : 0u);
-          mma_ts(tbase + kColO, wc + 16, bd, idO, 1u);
+          if constexpr (kLo) mma_ts(tbase + kColO, wc + 16, bd, idO, 1u);
         }
         tc_commit(bars + kBarPvDone + (jj & 1));
         // The slot is free once P.V is done: its score MMA completed before
@@ -1227,7 +1241,7 @@ int launch_tiles_t(const PrefillArgs &a, cudaStream_t st) {
 }
 
 // Tile and attention kernels of one wave.
-template <bool kWin>
+template <bool kWin, bool kLo>
 int launch_wave(const PrefillArgs &a, unsigned grid, cudaStream_t st) {
   int e;
   if (a.two_k && a.two_v) e = launch_tiles_t<true, true, kWin>(a, st);
@@ -1236,7 +1250,8 @@ int launch_wave(const PrefillArgs &a, unsigned grid, cudaStream_t st) {
   else e = launch_tiles_t<false, false, kWin>(a, st);
   if (e) return e;
   const AttnSmem L = attn_smem_layout(a.nslots);
-  const cudaError_t ce = ensure_max_dynamic_smem<prefill_kernel<kWin>>(static_cast<int>(L.total));
+  constexpr auto kern = prefill_kernel<kWin, kLo>;
+  const cudaError_t ce = ensure_max_dynamic_smem<kern>(static_cast<int>(L.total));
   if (ce != cudaSuccess) return static_cast<int>(ce);
   if constexpr (kWin) {
     // The attention kernel may start while the tile kernel runs: its loader
@@ -1251,9 +1266,9 @@ int launch_wave(const PrefillArgs &a, unsigned grid, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return static_cast<int>(cudaLaunchKernelEx(&cfg, prefill_kernel<kWin>, a));
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kern, a));
   } else {
-    prefill_kernel<kWin><<<grid, kAttnThreads, L.total, st>>>(a);
+    kern<<<grid, kAttnThreads, L.total, st>>>(a);
     return static_cast<int>(cudaGetLastError());
   }
 }
@@ -1293,8 +1308,9 @@ int launch_prefill_attention(const PrefillArgs &a, void *stream) {
     return static_cast<int>(cudaErrorInvalidValue);
   const int64_t grid = prefill_grid(a.nbh, a.G, a.n_q);
   if (grid < 1 || grid > 0x7FFFFFFF) return static_cast<int>(cudaErrorInvalidValue);
-  return a.window > 0 ? launch_wave<true>(a, static_cast<unsigned>(grid), st)
-                      : launch_wave<false>(a, static_cast<unsigned>(grid), st);
+  const unsigned n = static_cast<unsigned>(grid);
+  if (a.window == 0) return launch_wave<false, true>(a, n, st);
+  return a.out_dtype == DQ_F32 ? launch_wave<true, true>(a, n, st) : launch_wave<true, false>(a, n, st);
 }
 
 }  // namespace dqi

@@ -382,7 +382,8 @@ int dq_prefill_attention_paged(const dq_tables *t, const void *q, int q_dtype,
  *   sm_scale    must be positive
  * Out of range arguments give DQ_ERR_SHAPE. With window >= T_cap the result is
  * that of the call without a window (bit for bit, but for a decode step's fp32
- * outputs, which carry V's levels to 2^-22 here). A container whose fp16 norm is infinite
+ * outputs, which carry V's levels to 2^-22 here, and a chunk's bf16 outputs,
+ * whose softmax weights are single fp16 values). A container whose fp16 norm is infinite
  * or NaN (a corrupt one) counts in integrity_errors and its norm as 0, so it
  * cannot reach the queries that do not see it. Everything else is as in
  * dq_decode_attention[_paged] (p = length - 1; the workspace is

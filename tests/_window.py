@@ -9,7 +9,9 @@ then off by a factor of at most exp(2 d). P.V adds the relative error e_v of
 V's levels, the fp32 sums over n tokens (n + 64) 2^-24, the weights' and the
 exponential's 2^-20 in all, and (chunks) the fp16 halves' smallest step 2^-25
 per token times the largest level. fp32 outputs of a decode step carry V's
-levels in two fp16 parts, so e_v is 2^-22 there (the second part's rounding). Rotations keep the 2-norm, so each output
+levels in two fp16 parts, so e_v is 2^-22 there (the second part's rounding).
+bf16 outputs of a chunk carry the weights as single fp16 values, each rounded
+by at most 2^-11 of itself (or the half step 2^-25 counted above). Rotations keep the 2-norm, so each output
 coordinate is off by at most the sum of these times the largest visible ||v||.
 """
 from __future__ import annotations
@@ -34,7 +36,8 @@ def level_errors(stream, frequency_weighted):
     return err[j]
 
 
-def attention(tab, q, kcont, vcont, start, window, sinks, chunk, sm_scale=None, half_levels=True):
+def attention(tab, q, kcont, vcont, start, window, sinks, chunk, sm_scale=None, half_levels=True,
+              half_weights=False):
     """q [B, n, Hq, 128]; flat containers [B, Hkv, T_cap, C]; query i of
     sequence b at position start[b] + i (a position outside the cache gives 0).
     Returns (out, bound) with bound [B, n, Hq, 1]."""
@@ -78,6 +81,8 @@ def attention(tab, q, kcont, vcont, start, window, sinks, chunk, sm_scale=None, 
                 big = np.where(seen, nv, 0.0).max(1)
                 m = seen.sum(1)
                 bound[b, rows, h * G + g, 0] = big * (np.expm1(2 * d) + ev + (m + 64) * 2.0 ** -24 + 2.0 ** -20)
+                if half_weights:
+                    bound[b, rows, h * G + g, 0] += 2.0 ** -11 * big
                 if chunk:
                     bound[b, rows, h * G + g, 0] += 2.0 ** -25 * m * np.abs(tab.v.yf).max()
     return out, bound

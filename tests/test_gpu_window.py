@@ -239,8 +239,20 @@ def test_prefill_group_sizes_and_types(G, bits, q_dtype, out_dtype):
     n_q, start, window, sinks = 141, [459, 201], 133, 7
     q = _rounded(synth.q_chunk(w, n_q), q_dtype)
     got = _np(_prefill(lib, q, kc, vc, start, window, sinks, q_dtype, out_dtype))
-    want, bound = W.attention(ref, q, rk, rv, start, window, sinks, chunk=True)
+    want, bound = W.attention(ref, q, rk, rv, start, window, sinks, chunk=True, half_weights=out_dtype == BF16)
     W.assert_within(got, want, bound, out_dtype == BF16, "G %d" % G)
+
+
+def test_prefill_bf16_outputs_in_windows_long_and_short():
+    # One fp16 value per weight: many small weights, one large one, sinks far behind.
+    B, Hkv, G, T = 2, 2, 4, 900
+    w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T)
+    n_q, start = 130, [770, 300]
+    q = _rounded(synth.q_chunk(w, n_q), BF16)
+    for window, sinks, scale in ((1, 0, 1.0), (800, 0, 1.0), (64, 200, 0.01), (500, 3, 4.0)):
+        got = _np(_prefill(lib, q * np.float32(scale), kc, vc, start, window, sinks, F32, BF16))
+        want, bound = W.attention(ref, q * np.float32(scale), rk, rv, start, window, sinks, chunk=True, half_weights=True)
+        W.assert_within(got, want, bound, True, "window %d scale %g" % (window, scale))
 
 
 def test_prefill_rows_outside_the_cache():
