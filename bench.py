@@ -891,7 +891,8 @@ def prefill_launches_per_step(drift_mode):
 # pass) of `bench.py --prefill 512 --workload qwen3_8b_b16_t8k`: the decoded
 # tiles read once (545 MB) plus the queries, and the fp32 output. Reported
 # only for that workload and container size while the kernel source matches.
-# (The file has changed since that capture in comments only.)
+# (Since that capture the file has changed in comments and in the windowed
+# instances only.)
 PREFILL_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_prefill.cu", "sha256_16": "ae75fc9a99f72919",
                    "workload": "qwen3_8b_b16_t8k", "chunk": 512, "ck": 36, "cv": 36,
                    "bytes": 616.05e6 + 134.59e6}
