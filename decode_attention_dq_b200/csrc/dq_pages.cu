@@ -248,7 +248,7 @@ __device__ __forceinline__ void advance_item(const PagesArgs &a, long long it, l
   if (j0 == 0 && lane == 0) n_of.clamped += (raw != len || want != len2) ? 1 : 0;
   // Blocks [g_lo, g_hi) are given back; blocks [t_lo, t_hi) need a page.
   long long g_lo = 0, g_hi = n < 0 ? mp : 0;
-  if (n >= 0 && a.window > 0) {
+  if (n > 0 && a.window > 0) {  // (a row that gets no token may attend from its last one again)
     g_lo = (a.sinks + kPage - 1) / kPage;
     const long long seen = len + 1 - a.window;  // the first token that a next one sees
     g_hi = seen > 0 ? seen / kPage : 0;

@@ -22,7 +22,7 @@ def advance(refs, table, lens, n_new, window=0, sinks=0):
             if not 0 <= e < P:
                 count["bad"] += int(e != -1)
                 table[b, j] = -1
-            elif n < 0 or (window > 0 and PAGE * j >= sinks and PAGE * j + PAGE <= L + 1 - window):
+            elif n < 0 or (n > 0 and window > 0 and PAGE * j >= sinks and PAGE * j + PAGE <= L + 1 - window):
                 refs[e] -= 1
                 count["released"] += 1
                 table[b, j] = -1

@@ -131,6 +131,15 @@ def test_advance_out_of_range(tab):
         _same(_advance(tab, refs, table, lens, n, window, sinks), R.advance(refs, table, lens, n, window, sinks), "out of range")
 
 
+def test_a_row_without_new_tokens_keeps_what_its_last_one_sees(tab):
+    # Length 65, window 33: the last token's query sees tokens 32 .. 64, the next one's 33 .. 65 and no longer page 0.
+    table, refs = np.array([[4, 2, 0, -1]]), np.array([1, 0, 1, 0, 1])
+    for n, left in ((0, [4, 2, 0, -1]), (1, [-1, 2, 0, -1]), (-1, [-1] * 4)):
+        got = _advance(tab, refs, table, [65], [n], window=33)
+        _same(got, R.advance(refs, table, [65], [n], 33), "n %d" % n)
+        assert got[1].tolist() == [left]
+
+
 def test_advance_of_no_rows_counts_the_pool(tab):
     got = _advance(tab, [0, 1, 0, 0], np.zeros((0, 3)), [], [])
     _same(got, ([0, 1, 0, 0], np.zeros((0, 3)), [], dict.fromkeys(dq._native.PAGE_COUNT_FIELDS, 0) | dict(free_pages=3)), "no rows")
