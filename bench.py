@@ -61,9 +61,10 @@ LAUNCHES_PER_STEP = 4
 # scales with the token-heads a launch processes (reads are the containers,
 # writes the partial states). It belongs to one version of the kernel source:
 # for any other, or other container sizes, traffic is reported as null.
-# (The file has changed since that capture in comments only.)
+# (Since that capture the file has changed in comments and in the windowed
+# instances only.)
 DECODE_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_decode.cu",
-                  "sha256_16": "26d42a3180ecbf4b", "ck": 36, "cv": 36,
+                  "sha256_16": "b7bea06fb7063b17", "ck": 36, "cv": 36,
                   "bytes_per_token_head": (151.367680e6 + 3.288064e6) / (32 * 8 * 8192)}
 
 

@@ -200,6 +200,19 @@ __device__ __forceinline__ void score_fma(float (&sc)[G], const float *qi, float
   }
 }
 
+// Adds a run of coordinates' scores to the sums. With fp32 outputs of a
+// windowed call (kLo) each 8 coordinates are summed by themselves first: the
+// roundings of 128 additions to one sum would be most of the output's error
+// (5e-7 of it in the mean; a third of that so).
+template <int G>
+__device__ __forceinline__ void add_run(float (&sc)[G], float (&run)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    sc[g] = __fadd_rn(sc[g], run[g]);
+    run[g] = 0.0f;
+  }
+}
+
 // Byte offset in the V tile of token t's 16-byte chunk c (8 coordinates):
 // chunks are XOR-swizzled by t & 7, so a lane's 128-bit store of its own row
 // and an 8-row ldmatrix both touch 8 different 16-byte bank groups.
@@ -617,11 +630,13 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
       RansLane rk = rans_open(smem, static_cast<uint32_t>(kb - smem));
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
+      float run[G] = {};
 #pragma unroll 4
       for (int i = 0; i < kD; ++i) {
         const uint32_t ek = rans_step<kTwoK>(rk, lut_k, smem);
         const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(ek));
-        score_fma<G>(sc, qt + i * G, yk);
+        score_fma<G>(kLo ? run : sc, qt + i * G, yk);
+        if (kLo && i % 8 == 7) add_run<G>(sc, run);
       }
       const bool valid = visible(group_t0(0));
       count_bad(valid, rk, kb);
@@ -666,14 +681,16 @@ __global__ void __launch_bounds__(max_warps_for(G) * 32, 1) decode_split_kernel(
         for (int i8 = 0; i8 < kCoords; i8 += 8) {
           uint32_t hv[8];
           if (has_next) {
+            float run[G] = {};
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const int i = part * kCoords + i8 + u;
               const uint32_t ek = rans_step<kTwoK>(rk, lut_k, smem);
               hv[u] = rans_step<kTwoV>(rv, lut_v, smem);
               const float yk = *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(ek));
-              score_fma<G>(sc, qt + i * G, yk);
+              score_fma<G>(kLo ? run : sc, qt + i * G, yk);
             }
+            if constexpr (kLo) add_run<G>(sc, run);
           } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -993,10 +1010,13 @@ __global__ void __launch_bounds__(kFewGroups * 64, 1) decode_few_kernel(const De
       float sc[G];
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) sc[gg] = 0.0f;
+      float run[G] = {};
 #pragma unroll 8
       for (int i = 0; i < kD; ++i) {
         const uint32_t e = rans_step<kTwo>(rl, lut_k, smem);
-        score_fma<G>(sc, qt + i * G, *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(e)));
+        score_fma<G>(kLo ? run : sc, qt + i * G,
+                     *reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(lev) + level_offset(e)));
+        if (kLo && i % 8 == 7) add_run<G>(sc, run);
       }
       const float nk = finite_norm_of(cb), nv = finite_norm_of(gsm + L.vst + lane);
 #pragma unroll
