@@ -253,7 +253,8 @@ __device__ __forceinline__ void advance_item(const PagesArgs &a, long long it, l
     const long long seen = len + 1 - a.window;  // the first token that a next one sees
     g_hi = seen > 0 ? seen / kPage : 0;
   }
-  const long long t_lo = n < 0 ? 0 : len / kPage, t_hi = n < 0 ? 0 : (len2 + kPage - 1) / kPage;
+  const bool grows = n > 0 && len2 > len;
+  const long long t_lo = grows ? len / kPage : 0, t_hi = grows ? (len2 + kPage - 1) / kPage : 0;
   int32_t *out = a.table_out + b * mp;
   int need = 0;
   for_quads(a.table_in + b * mp, j0, j1, vec, -1, [&](long long j, const int (&e)[4]) {

@@ -461,12 +461,16 @@ size_t dq_pages_workspace_bytes(const dq_tables *t, int64_t num_pages, int B,
 /* Makes room for the next tokens of every sequence and gives back what none
  * of them sees. With L = d_lens[b] and n = d_n_new[b]:
  *   n < 0    the sequence ends: all its references go, its new length is 0
- *   n = 0    the row stays as it is
+ *   n = 0    the row stays as it is (entries out of range become -1 and a
+ *            length out of range is clamped, as in every row)
  *   n > 0    its new length is L + n (at most 32 max_pages, else clamped).
  *            With window > 0 the pages that lie wholly in [sinks, L + 1 -
  *            window) go: no query from position L on sees them (see
  *            dq_decode_attention_window). Then every entry without a page
- *            among those of tokens L .. L + n - 1 gets one.
+ *            among those of tokens L .. L + n - 1 gets one. (So does the block
+ *            of token L where it holds earlier tokens but has lost its page, in
+ *            a state that a call wrote which ran short: the page handed out
+ *            then does not hold those tokens. Go back to the state before.)
  * Pages are handed out after all releases, lowest free page first, in the
  * order of the rows and of their entries. window 0 keeps everything. Each
  * output may be the input itself. */
