@@ -146,6 +146,16 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
+def _workspace_for(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace that lives for one call, from the pool of the stream that
+    the call runs on: a block of another stream's pool may still be in use by
+    work queued there, and may be handed to such work before the call has run."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return DQ_F32
@@ -278,7 +288,7 @@ def dq_append_kv(tab: Tables, k: torch.Tensor, v: torch.Tensor, start_pos: torch
         return
     if workspace is None:
         nbytes = dq_append_workspace_bytes(tab, B, Hkv, n_new)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=kcache.device)
+        workspace = _workspace_for(max(nbytes, 16), kcache.device, stream)
     _check("dq_append_kv_ws", load().dq_append_kv_ws(
         tab.handle, _ptr(k), _ptr(v), _dtype_code(k), B, Hkv, n_new, _ptr(start_pos),
         _ptr(kcache), _ptr(vcache), T_cap, _ptr(workspace), workspace.numel(), _ptr(stats),
@@ -329,10 +339,9 @@ def dq_prefill_workspace_bytes(tab: Tables, B: int, Hkv: int, T_cap: int) -> int
     return int(load().dq_prefill_workspace_bytes(tab.handle, B, Hkv, T_cap))
 
 
-def _prefill_ws(tab, workspace, B, Hkv, T_cap, device):
-    need = dq_prefill_workspace_bytes(tab, B, Hkv, T_cap)
+def _prefill_ws(tab, workspace, B, Hkv, T_cap, device, stream):
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _workspace_for(dq_prefill_workspace_bytes(tab, B, Hkv, T_cap), device, stream)
     return workspace
 
 
@@ -350,7 +359,7 @@ def dq_prefill_attention(tab: Tables, q: torch.Tensor, kcache: torch.Tensor, vca
     assert out.shape == q.shape
     if sm_scale is None:
         sm_scale = 128 ** -0.5
-    workspace = _prefill_ws(tab, workspace, B, Hkv, T_cap, q.device)
+    workspace = _prefill_ws(tab, workspace, B, Hkv, T_cap, q.device, stream)
     _check("dq_prefill_attention", load().dq_prefill_attention(
         tab.handle, _ptr(q), _dtype_code(q), _ptr(kcache), _ptr(vcache), _ptr(q_start), B, n_q, Hq,
         Hkv, T_cap, float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
@@ -368,7 +377,7 @@ def dq_prefill_attention_paged(tab: Tables, q: torch.Tensor, kpool: torch.Tensor
     assert page_table.dtype == torch.int32 and page_table.is_contiguous() and out.shape == q.shape
     if sm_scale is None:
         sm_scale = 128 ** -0.5
-    workspace = _prefill_ws(tab, workspace, B, Hkv, 32 * page_table.shape[1], q.device)
+    workspace = _prefill_ws(tab, workspace, B, Hkv, 32 * page_table.shape[1], q.device, stream)
     _check("dq_prefill_attention_paged", load().dq_prefill_attention_paged(
         tab.handle, _ptr(q), _dtype_code(q), _ptr(kpool), _ptr(vpool), kpool.shape[0],
         _ptr(page_table), page_table.shape[1], _ptr(q_start), B, n_q, Hq, Hkv, float(sm_scale),
@@ -496,11 +505,12 @@ def dq_prefill_attention_window(tab: Tables, q: torch.Tensor, kcache: torch.Tens
     if q.numel() == 0:
         return
     if workspace is None:
-        workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kcache.shape[1], kcache.shape[2], n_q,
-                                                                  window, sinks), dtype=torch.uint8, device=q.device)
-    if stream is not None:  # (the caller may drop it, or has left it to this call, before the kernels run)
-        workspace.record_stream(stream)
-    _check_cuda("q workspace", q, workspace)
+        workspace = _workspace_for(dq_prefill_window_workspace_bytes(tab, B, kcache.shape[1], kcache.shape[2], n_q,
+                                                                     window, sinks), q.device, stream)
+    else:
+        _check_cuda("q workspace", q, workspace)
+        if stream is not None:  # (the caller may drop it before the kernels run)
+            workspace.record_stream(stream)
     _check("dq_prefill_attention_window", load().dq_prefill_attention_window(
         tab.handle, q.data_ptr(), _dtype_code(q), kcache.data_ptr(), vcache.data_ptr(), q_start.data_ptr(), B, n_q, Hq, kcache.shape[1],
         kcache.shape[2], window, sinks, float(128 ** -0.5 if sm_scale is None else sm_scale), out.data_ptr(),
@@ -524,12 +534,12 @@ def dq_prefill_attention_window_paged(tab: Tables, q: torch.Tensor, kpool: torch
     if q.numel() == 0:
         return
     if workspace is None:
-        workspace = torch.empty(dq_prefill_window_workspace_bytes(tab, B, kpool.shape[1], 32 * page_table.shape[1],
-                                                                  n_q, window, sinks),
-                                dtype=torch.uint8, device=q.device)
-    if stream is not None:  # (the caller may drop it, or has left it to this call, before the kernels run)
-        workspace.record_stream(stream)
-    _check_cuda("q workspace", q, workspace)
+        workspace = _workspace_for(dq_prefill_window_workspace_bytes(tab, B, kpool.shape[1], 32 * page_table.shape[1],
+                                                                     n_q, window, sinks), q.device, stream)
+    else:
+        _check_cuda("q workspace", q, workspace)
+        if stream is not None:  # (the caller may drop it before the kernels run)
+            workspace.record_stream(stream)
     _check("dq_prefill_attention_window_paged", load().dq_prefill_attention_window_paged(
         tab.handle, q.data_ptr(), _dtype_code(q), kpool.data_ptr(), vpool.data_ptr(), kpool.shape[0], page_table.data_ptr(),
         page_table.shape[1], q_start.data_ptr(), B, n_q, Hq, kpool.shape[1], window, sinks,
@@ -687,7 +697,7 @@ def dq_append_kv_paged(tab: Tables, k: torch.Tensor, v: torch.Tensor, start_pos:
     assert page_table.dtype == torch.int32 and page_table.is_contiguous() and page_table.shape[0] == B
     if workspace is None:
         nbytes = dq_append_workspace_bytes(tab, B, Hkv, n_new)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=kpool.device)
+        workspace = _workspace_for(max(nbytes, 16), kpool.device, stream)
     _check("dq_append_kv_paged", load().dq_append_kv_paged(
         tab.handle, _ptr(k), _ptr(v), _dtype_code(k), B, Hkv, n_new, _ptr(start_pos),
         _ptr(kpool), _ptr(vpool), kpool.shape[0], _ptr(page_table), page_table.shape[1],
