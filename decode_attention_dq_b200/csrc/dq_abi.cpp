@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -715,6 +716,38 @@ size_t dq_pages_workspace_bytes(const dq_tables *t, int64_t num_pages, int B, in
   return dqi::pages_layout(num_pages, B, max_pages).total;
 }
 
+// An array of the bookkeeping calls.
+struct Span {
+  const void *p;
+  int64_t bytes;
+};
+static bool share_bytes(const Span &a, const Span &b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) &&
+         y < x + static_cast<uintptr_t>(a.bytes);
+}
+// The kernels read their inputs again after they have begun to write: an
+// output shares no byte with an input or with another output, but for the
+// first `own` of them, which may be the input of the same index itself.
+static int check_apart(std::initializer_list<Span> in, std::initializer_list<Span> out, size_t own) {
+  for (size_t o = 0; o < out.size(); ++o) {
+    const Span &x = out.begin()[o];
+    for (size_t i = 0; i < in.size(); ++i)
+      if (share_bytes(x, in.begin()[i]) && !(i == o && i < own && x.p == in.begin()[i].p)) return DQ_ERR_SHAPE;
+    for (size_t i = 0; i < o; ++i)
+      if (share_bytes(x, out.begin()[i])) return DQ_ERR_SHAPE;
+  }
+  return DQ_OK;
+}
+// Bytes of int32 arrays (0 for sizes that pages_args refuses) and of the workspace that is used.
+static int64_t int_bytes(int64_t rows, int64_t each) {
+  return rows > 0 && rows <= 0x7FFFFFFF && each > 0 && each <= 2 * kMaxTablePages ? 4 * rows * each : 0;
+}
+static int64_t used_bytes(int64_t num_pages, int64_t max_pages, int B, size_t ws_bytes) {
+  if (num_pages < 1 || num_pages > 0x7FFFFFFF || max_pages < 1 || max_pages > kMaxTablePages || B < 0) return 0;
+  return static_cast<int64_t>(std::min(ws_bytes, dqi::pages_layout(num_pages, B, max_pages).total));
+}
+
 // Checks and arguments that the bookkeeping calls share; rows of the old and
 // the new table. Arrays of no rows may be NULL.
 static int pages_args(const dq_tables *t, int64_t num_pages, int64_t max_pages, const int32_t *d_refs,
@@ -760,9 +793,16 @@ int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_ref
     if (B > 0 && (!d_lens || !d_n_new || !d_lens_out)) return DQ_ERR_NULL;
     if (window < 0 || sinks < 0) return DQ_ERR_SHAPE;
     if (!aligned(d_lens, 4) || !aligned(d_n_new, 4) || !aligned(d_lens_out, 4)) return DQ_ERR_ALIGN;
+    const int64_t refs = int_bytes(num_pages, 1), rows = int_bytes(B, 1), table = int_bytes(B, max_pages);
+    // (n_new may be lens_out: a row's number is read by the thread that then writes its length.)
+    int rc = check_apart({{d_refs, refs}, {d_page_table, table}, {d_lens, rows}, {d_n_new, d_n_new == d_lens_out ? 0 : rows}},
+                         {{d_refs_out, refs}, {d_page_table_out, table}, {d_lens_out, rows}, {d_counts, sizeof(dq_page_counts)},
+                          {d_workspace, used_bytes(num_pages, max_pages, B, ws_bytes)}},
+                         3);
+    if (rc != DQ_OK) return rc;
     dqi::PagesArgs a;
-    const int rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B, d_refs_out, d_page_table_out, B,
-                              reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
+    rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B, d_refs_out, d_page_table_out, B,
+                    reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
     if (rc != DQ_OK) return rc;
     a.lens_in = d_lens;
     a.step = d_n_new;
@@ -784,12 +824,16 @@ int dq_pages_fork(const dq_tables *t, int64_t num_pages, const int32_t *d_refs, 
     if ((B_in > 0 && !d_lens) || (B_out > 0 && (!d_parent || !d_lens_out || !d_pairs))) return DQ_ERR_NULL;
     if (!aligned(d_lens, 4) || !aligned(d_parent, 4) || !aligned(d_lens_out, 4) || !aligned(d_pairs, 4))
       return DQ_ERR_ALIGN;
-    // The new rows are read from the old ones in any order.
-    if (d_refs && d_refs == d_refs_out) return DQ_ERR_SHAPE;
-    if (B_in > 0 && B_out > 0 && (d_page_table == d_page_table_out || d_lens == d_lens_out)) return DQ_ERR_SHAPE;
+    const int64_t refs = int_bytes(num_pages, 1), rows = int_bytes(B_out, 1);
+    int rc = check_apart({{d_refs, refs}, {d_page_table, int_bytes(B_in, max_pages)}, {d_lens, int_bytes(B_in, 1)}, {d_parent, rows}},
+                         {{d_refs_out, refs}, {d_page_table_out, int_bytes(B_out, max_pages)}, {d_lens_out, rows},
+                          {d_pairs, int_bytes(B_out, 2)}, {d_counts, sizeof(dq_page_counts)},
+                          {d_workspace, used_bytes(num_pages, max_pages, std::max(B_in, B_out), ws_bytes)}},
+                         0);
+    if (rc != DQ_OK) return rc;
     dqi::PagesArgs a;
-    const int rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B_in, d_refs_out, d_page_table_out, B_out,
-                              reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
+    rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B_in, d_refs_out, d_page_table_out, B_out,
+                    reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
     if (rc != DQ_OK) return rc;
     a.lens_in = d_lens;
     a.step = d_parent;
@@ -808,9 +852,15 @@ int dq_pages_compact(const dq_tables *t, int64_t num_pages, const int32_t *d_ref
   try {
     if (!d_pairs) return DQ_ERR_NULL;
     if (!aligned(d_pairs, 4)) return DQ_ERR_ALIGN;
+    const int64_t refs = int_bytes(num_pages, 1), table = int_bytes(B, max_pages);
+    int rc = check_apart({{d_refs, refs}, {d_page_table, table}},
+                         {{d_refs_out, refs}, {d_page_table_out, table}, {d_pairs, int_bytes(std::max<int64_t>(1, num_pages / 2), 2)},
+                          {d_counts, sizeof(dq_page_counts)}, {d_workspace, used_bytes(num_pages, max_pages, B, ws_bytes)}},
+                         2);
+    if (rc != DQ_OK) return rc;
     dqi::PagesArgs a;
-    const int rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B, d_refs_out, d_page_table_out, B,
-                              reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
+    rc = pages_args(t, num_pages, max_pages, d_refs, d_page_table, B, d_refs_out, d_page_table_out, B,
+                    reinterpret_cast<int32_t *>(d_counts), d_workspace, ws_bytes, &a);
     if (rc != DQ_OK) return rc;
     a.pairs = d_pairs;
     const int e = dqi::launch_pages_compact(a, stream);

@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
             need += copy ? 1 : 0;
             a.item_need[row] = copy ? 1 : 0;
             a.item_lo[row] = v[k];  // the page to copy from
+            a.item_hi[row] = static_cast<int32_t>(col);
             if (copy) v[k] = -1;
           }
         } else if (held) {
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
       const int page = __ldcg(a.list + r);
       a.pairs[2 * r] = __ldcg(a.item_lo + c);
       a.pairs[2 * r + 1] = page;
-      a.table_out[c * mp + clamp_tokens(a.lens_in[a.step[c]], cap) / kPage] = page;
+      a.table_out[c * mp + __ldcg(a.item_hi + c)] = page;
     }
   }
   // (Counted at the end: atomics that return what a page had before would

@@ -442,8 +442,10 @@ int dq_prefill_attention_window_paged(const dq_tables *t, const void *q, int q_d
  *               be initialised; calls sharing it must not overlap on the GPU
  * A table entry outside [0, num_pages) other than -1 counts in `bad` and is
  * -1 in the new table; a length outside [0, 32 max_pages] is clamped and
- * counted. Arrays of no rows may be NULL. Errors: DQ_ERR_NULL, _SHAPE, _ALIGN
- * (4 bytes; workspace 16), _WORKSPACE, _DEVICE, _CUDA. */
+ * counted. Arrays of no rows may be NULL. An output shares no memory with an
+ * input or another output, but where a call lets it be its own input
+ * (DQ_ERR_SHAPE). Errors: DQ_ERR_NULL, _SHAPE, _ALIGN (4 bytes; workspace 16),
+ * _WORKSPACE, _DEVICE, _CUDA. */
 typedef struct {
   int32_t free_pages; /* pages without a reference after the call            */
   int32_t taken;      /* pages handed out                                    */
@@ -472,8 +474,8 @@ size_t dq_pages_workspace_bytes(const dq_tables *t, int64_t num_pages, int B,
  *            a state that a call wrote which ran short: the page handed out
  *            then does not hold those tokens. Go back to the state before.)
  * Pages are handed out after all releases, lowest free page first, in the
- * order of the rows and of their entries. window 0 keeps everything. Each
- * output may be the input itself. */
+ * order of the rows and of their entries. window 0 keeps everything.
+ * d_refs_out, d_page_table_out and d_lens_out may be their inputs. */
 int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
                      const int32_t *d_page_table, int64_t max_pages,
                      const int32_t *d_lens, const int32_t *d_n_new, int B,
@@ -489,8 +491,8 @@ int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_ref
  * (the children will write to it): the parent's first child keeps it, if the
  * parent's row had its only reference; every other child gets the lowest free
  * page of the old state, and d_pairs [B_out][2] the copy to make (source,
- * destination; then -1, -1). Where pages run short the entry is -1. Outputs
- * must not be inputs (DQ_ERR_SHAPE). dq_pages_copy makes the copies, before
+ * destination; then -1, -1). Where pages run short the entry is -1. No output
+ * may be an input, d_parent included. dq_pages_copy makes the copies, before
  * the next append. */
 int dq_pages_fork(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
                   const int32_t *d_page_table, int64_t max_pages,
@@ -504,8 +506,8 @@ int dq_pages_fork(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
  * order. d_pairs [max(1, num_pages / 2)][2] lists the moves (then -1, -1);
  * refs and table are renumbered (an entry whose page has no reference becomes
  * -1). References that the caller holds outside the table are the caller's to
- * renumber. Each output may be the input itself. dq_pages_copy makes the
- * moves; sources and destinations are disjoint. */
+ * renumber. d_refs_out and d_page_table_out may be their inputs. dq_pages_copy
+ * makes the moves; sources and destinations are disjoint. */
 int dq_pages_compact(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
                      const int32_t *d_page_table, int64_t max_pages, int B,
                      int32_t *d_refs_out, int32_t *d_page_table_out,
