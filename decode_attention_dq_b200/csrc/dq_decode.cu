@@ -987,17 +987,17 @@ __global__ void __launch_bounds__(kFewGroups * 64, 1) decode_few_kernel(const De
   __syncthreads();
   // The tables have landed (bounded: a wait that gives up counts, and the
   // sequence's tokens in this CTA are left out).
-  bool ready = false;
-  for (uint32_t it = 0; it < (1u << 24) && !ready; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred P;\nmbarrier.try_wait.parity.shared::cta.b64 P, [%1], 0;\nselp.u32 %0, 1, 0, P;\n}\n"
-        : "=r"(ok)
-        : "r"(bar)
-        : "memory");
-    ready = ok != 0;
-  }
-  ready = __syncthreads_and(ready);
+  auto landed = [&]() {
+    uint32_t ok = 0;
+    for (uint32_t it = 0; it < (1u << 24) && !ok; ++it)
+      asm volatile(
+          "{\n.reg .pred P;\nmbarrier.try_wait.parity.shared::cta.b64 P, [%1], 0;\nselp.u32 %0, 1, 0, P;\n}\n"
+          : "=r"(ok)
+          : "r"(bar)
+          : "memory");
+    return ok != 0;
+  };
+  const bool ready = __syncthreads_and(landed());
 
   unsigned bad_count = 0, over_count = 0;
   if (mine && ready) {
@@ -1121,6 +1121,9 @@ __global__ void __launch_bounds__(kFewGroups * 64, 1) decode_few_kernel(const De
     for (int k = 0; k < 4; ++k)
       store_elem(a.out, row * kD + lane + 32 * k, apply_sign(o[k] * inv, __ldg(a.sign_bits + h * 4 + k), lane), a.out_dtype);
   }
+  // A CTA that gave up waits (again with a limit) for its copies: this shared
+  // memory is another CTA's after it.
+  if (!ready && threadIdx.x == 0) landed();
   if (a.stats && lane == 0) {
     if (bad_count) atomicAdd(&a.stats->integrity_errors, static_cast<unsigned long long>(bad_count));
     if (bad_pages) atomicAdd(&a.stats->bad_pages, static_cast<unsigned long long>(bad_pages));
