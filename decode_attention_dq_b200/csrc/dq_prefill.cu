@@ -67,8 +67,9 @@
 // saved a third of the set-up but spilled in the block loop (96 registers) and
 // were 3 % slower.
 // bf16 outputs of a windowed chunk take the weights W as single fp16 values
-// (kLo false): each is off by at most 2^-11 of itself, 2.8e-4 of the output in
-// the mean against the output's own 1.7e-3, P.V is half as many MMAs and the
+// (kLo false): each is off by at most 2^-11 of itself (by 2^-25 below 2^-14,
+// with hi + lo too), 2e-4 of the output in the mean against the output's own
+// 1.7e-3, P.V is half as many MMAs and the
 // softmax warps, which set the pace, have less to do per weight (3.1 thousand
 // cycles a block, 3.3 with hi + lo, at a higher clock; 16 sequences x 512 tokens x 8
 // KV heads, G = 4, window 1024: 445 us, 482 with hi + lo; 4 x 2048 tokens, G =

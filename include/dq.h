@@ -381,9 +381,14 @@ int dq_prefill_attention_paged(const dq_tables *t, const void *q, int q_dtype,
  *   sinks       first tokens that every query sees, >= 0
  *   sm_scale    must be positive
  * Out of range arguments give DQ_ERR_SHAPE. With window >= T_cap the result is
- * that of the call without a window (bit for bit, but for a decode step's fp32
- * outputs, which carry V's levels to 2^-22 here, and a chunk's bf16 outputs,
- * whose softmax weights are single fp16 values). A container whose fp16 norm is infinite
+ * that of the call without a window: bit for bit for a chunk's fp32 outputs; but
+ * for the order of the fp32 sums, so that a bf16 value may round the other way,
+ * for a decode step's bf16 outputs. A decode step's fp32 outputs are closer to
+ * the definition here (V's levels to 2^-22), a chunk's bf16 outputs take single
+ * fp16 values as softmax weights. (A weight is the token's ||v|| times its
+ * exponential, which is 1 for the row's largest score: here it is held to 2^-11
+ * of itself, in two fp16 values to 2^-22 everywhere else, and never finer than
+ * 2^-25.) A container whose fp16 norm is infinite
  * or NaN (a corrupt one) counts in integrity_errors and its norm as 0, so it
  * cannot reach the queries that do not see it. Everything else is as in
  * dq_decode_attention[_paged] (p = length - 1; the workspace is

@@ -6,6 +6,8 @@ import pytest
 import torch
 
 import decode_attention_dq_b200 as dq
+from tests import _common as cm
+from tests import _window as W
 from tests.test_gpu_window import BF16, F32, _decode, _ints, _np, _prefill, _rounded, _setup, _workspace
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +36,18 @@ def test_calls_with_different_tables_one_behind_the_other():
         assert all(torch.equal(x, out) for x in outs)
         s = dq.stats_dict(stats)
         assert s["integrity_errors"] == 0 and s["wait_timeouts"] == 0
+
+
+@pytest.mark.parametrize("B,Hkv,T", [(1, 8, 1100), (40, 8, 170)])  # a cluster per (b, h); the balanced split
+def test_a_window_of_everything_agrees_but_for_the_order_of_sums(B, Hkv, T):
+    # Both calls are within the bound of the definition; so they differ by two bounds and a bf16 step at most.
+    G = 4
+    w, lib, ref, kc, vc, rk, rv = _setup(B, Hkv, G, T)
+    lens = [max(1, T - 9 * b) for b in range(B)]
+    q = _rounded(dq.synth.q_block(w), BF16)
+    got = _np(_decode(lib, q, kc, vc, lens, 2 ** 40, 0, dtype=BF16))
+    full = cm.gpu_attention(lib, q, kc, vc, lens, T_max=kc.shape[2], q_dtype=BF16, out_dtype=BF16)
+    want, bound = (x[:, 0] for x in W.attention(ref, q[:, None], rk, rv, np.array(lens) - 1, T, 0, chunk=False))
+    W.assert_within(got, want, bound, True, "windowed")
+    W.assert_within(full, want, bound, True, "without a window")
+    assert np.all(np.abs(got - full) <= 2 * bound + 2.0 ** -7 * (np.abs(want) + bound))
