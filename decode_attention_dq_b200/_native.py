@@ -411,8 +411,12 @@ def _check_int32(names: str, *pairs) -> None:
 
 
 def _check_stats(stats) -> None:
-    if stats is not None:
-        _check_cuda("stats", stats)
+    """None, or room for a dq_stats on the current device (the kernels add to its fields)."""
+    if stats is None:
+        return
+    if stats.nbytes < 8 * len(STATS_FIELDS) or stats.data_ptr() % 8:
+        raise ValueError("stats must hold %d 64-bit counters (new_stats), got %s %s" % (len(STATS_FIELDS), stats.dtype, tuple(stats.shape)))
+    _check_cuda("stats", stats)
 
 
 def _check_heads(q, out, kcache, vcache) -> None:

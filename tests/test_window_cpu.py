@@ -68,3 +68,13 @@ def test_binding_refuses_shapes_that_do_not_fit():
             N._check_heads(*args)
     with pytest.raises(ValueError, match="caches"):
         N._check_shapes("caches", cache, cache[:, :, :16], (1, 1, 32, 36), (1, 1, 32, 36))
+
+
+@pytest.mark.parametrize("small", [torch.zeros(13, dtype=torch.int64), torch.zeros(14, dtype=torch.int32),
+                                   torch.zeros(0, dtype=torch.int64)])
+def test_binding_refuses_counters_without_room(small):
+    with pytest.raises(ValueError, match="counters"):
+        N._check_stats(small)
+    with pytest.raises(ValueError, match="CUDA"):  # large enough, but not on a GPU
+        N._check_stats(dq.new_stats(device="cpu"))
+    N._check_stats(None)
