@@ -453,9 +453,9 @@ size_t dq_decode_workspace_bytes(const dq_tables *t, int B, int Hq, int Hkv, int
 }
 
 // Window arguments: at least the query's own token is visible, and scores are
-// masked before they are scaled.
+// masked before they are scaled (an infinite scale would give NaN weights).
 static int check_window(int64_t window, int64_t sinks, float sm_scale) {
-  return window < 1 || sinks < 0 || !(sm_scale > 0.0f) ? DQ_ERR_SHAPE : DQ_OK;
+  return window < 1 || sinks < 0 || !(sm_scale > 0.0f) || std::isinf(sm_scale) ? DQ_ERR_SHAPE : DQ_OK;
 }
 
 // Shared by the dq_decode_attention calls (page_table NULL: contiguous cache;

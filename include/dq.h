@@ -379,7 +379,7 @@ int dq_prefill_attention_paged(const dq_tables *t, const void *q, int q_dtype,
  * the attention are those of the calls above.
  *   window      tokens up to and including the query's own, >= 1
  *   sinks       first tokens that every query sees, >= 0
- *   sm_scale    must be positive
+ *   sm_scale    must be positive and finite
  * Out of range arguments give DQ_ERR_SHAPE. With window >= T_cap the result is
  * that of the call without a window: bit for bit for a chunk's fp32 outputs; but
  * for the order of the fp32 sums, so that a bf16 value may round the other way,

@@ -78,3 +78,10 @@ def test_binding_refuses_counters_without_room(small):
     with pytest.raises(ValueError, match="CUDA"):  # large enough, but not on a GPU
         N._check_stats(dq.new_stats(device="cpu"))
     N._check_stats(None)
+
+
+@pytest.mark.parametrize("call", [_decode, _prefill])
+def test_an_infinite_scale_is_refused(call):
+    assert call(N.load(), scale=float("inf")) == SHAPE
+    assert call(N.load(), paged=True, table=ctypes.c_void_p(4096), scale=float("inf")) == SHAPE
+    assert call(N.load(), scale=3e38) == NULL
