@@ -598,9 +598,9 @@ def dq_pages_fork(tab: Tables, refs: torch.Tensor, page_table: torch.Tensor, len
                   lens_out: torch.Tensor, pairs: torch.Tensor, counts: torch.Tensor, workspace: torch.Tensor,
                   stream=None) -> None:
     """Row c of the new table [B_out, max_pages] is row parent[c] of the old
-    one (negative: empty). Pages are shared; pairs [B_out, 2] lists the copies
-    of partly filled last pages for dq_pages_copy. Outputs must be other
-    tensors than the inputs."""
+    one (negative: empty). Pages are shared, but for those that the row will
+    write to; pairs [B_out, 2] lists the copies of partly filled last pages for
+    dq_pages_copy. Outputs must be other tensors than the inputs."""
     _check_cuda("refs page_table lens parent refs_out page_table_out lens_out pairs counts workspace", refs, page_table,
                 lens, parent, refs_out, page_table_out, lens_out, pairs, counts, workspace)
     B, max_pages = rows = page_table.shape

@@ -7,7 +7,8 @@
 //   advance  gives back what a sequence no longer needs and hands out the
 //            pages of its next tokens
 //   fork     row c of the new table is row parent[c] of the old one; full
-//            pages are shared, a partly filled last page is copied
+//            pages are shared, a partly filled last page is copied, pages past
+//            the length go to the first child
 //   compact  moves the live pages to the lowest numbers
 // Pages are handed out lowest first, in the order of the rows, and holes are
 // filled in ascending order, so every result is determined by the state:
@@ -432,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
   const long long mine = count_free(a.refs_in, w_lo, w_hi, vec_refs);
   cl.sync();
 
-  // Whether a row's last page t stays with its first child: nobody else may
-  // hold it.
+  // Whether a page t that the row will write to stays with its first child:
+  // nobody else may hold it.
   auto stays = [&](int t) { return __ldcg(a.refs_in + t) == 1; };
   // The old rows' references go, the children's come (items of all rows, over
   // the cluster); then the new rows (those whose new pages this CTA hands out,
@@ -446,10 +447,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
     const bool real = parent >= 0 && parent < a.B_in;
     const int raw = real ? a.lens_in[parent] : 0;
     const long long len = clamp_tokens(raw, cap);
-    const long long col = len % kPage ? len / kPage : -1;  // the partly filled block
+    // Blocks from own_lo on are written to as the row grows: the partly filled
+    // one (col), then those that lie past the length.
+    const long long own_lo = len / kPage, col = len % kPage ? own_lo : -1;
     if (!is_new && seg == 0 && lane == 0 && raw != len) ++clamped;
     const int kids = real ? __ldcg(a.children + parent) : 0;
-    if (!is_new && kids == 1 && !(col >= j0 && col < j1)) return;  // its pages keep their references
+    if (!is_new && kids == 1 && j1 <= own_lo) return;  // its pages keep their references
     const bool is_first = is_new && real && __ldcg(a.first + parent) == row;
     int32_t *out = a.table_out + row * mp;
     if (!real) {  // a row without a parent (there may be no old table at all)
@@ -464,20 +467,20 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PagesArgs a) {
       int v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool held = e[k] >= 0 && e[k] < P, last = j + k == col;
+        const bool held = e[k] >= 0 && e[k] < P, own = j + k >= own_lo;
         v[k] = held ? e[k] : -1;
         if (is_new) {
           bad += (!held && e[k] != -1) ? 1 : 0;
-          if (last) {
-            const bool copy = held && !(is_first && stays(e[k]));
-            need += copy ? 1 : 0;
-            a.item_need[row] = copy ? 1 : 0;
+          const bool leave = held && own && !(is_first && stays(e[k]));
+          if (j + k == col) {
+            need += leave ? 1 : 0;
+            a.item_need[row] = leave ? 1 : 0;
             a.item_lo[row] = v[k];  // the page to copy from
             a.item_hi[row] = static_cast<int32_t>(col);
-            if (copy) v[k] = -1;
           }
+          if (leave) v[k] = -1;
         } else if (held) {
-          const int d = last ? (kids > 0 && stays(e[k]) ? 0 : -1) : kids - 1;
+          const int d = own ? (kids > 0 && stays(e[k]) ? 0 : -1) : kids - 1;
           if (d) atomicAdd(a.refs_out + e[k], d);
         }
       }

@@ -479,7 +479,10 @@ size_t dq_pages_workspace_bytes(const dq_tables *t, int64_t num_pages, int B,
  *            a state that a call wrote which ran short: the page handed out
  *            then does not hold those tokens. Go back to the state before.)
  * Pages are handed out after all releases, lowest free page first, in the
- * order of the rows and of their entries. window 0 keeps everything.
+ * order of the rows and of their entries. window 0 keeps everything. A block
+ * that has a page keeps it, whoever else holds it: a caller who takes tokens
+ * back goes no further than to a block that the row holds alone, and passes a
+ * window larger by as many tokens, so that what the shorter row sees is there.
  * d_refs_out, d_page_table_out and d_lens_out may be their inputs. */
 int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
                      const int32_t *d_page_table, int64_t max_pages,
@@ -492,11 +495,14 @@ int dq_pages_advance(const dq_tables *t, int64_t num_pages, const int32_t *d_ref
 /* Forks sequences: row c of the new table is old row d_parent[c], with its
  * length; a negative parent gives an empty row (one of B_in or more too, and
  * counts in `bad`). Old rows that are nobody's parent are thereby dropped.
- * Pages are shared, except for a row's last page where it is partly filled
- * (the children will write to it): the parent's first child keeps it, if the
- * parent's row had its only reference; every other child gets the lowest free
- * page of the old state, and d_pairs [B_out][2] the copy to make (source,
- * destination; then -1, -1). Where pages run short the entry is -1. No output
+ * Pages are shared, except for those that the children will write to: a row's
+ * last page where it is partly filled, and pages past its length (a caller who
+ * takes tokens back by a smaller length leaves such pages). The parent's first
+ * child keeps them, if the parent's row had their only reference; every other
+ * child gets, for the partly filled one, the lowest free page of the old state,
+ * and d_pairs [B_out][2] the copy to make (source, destination; then -1, -1),
+ * and -1 for the others. Where pages run short the entry is -1. An entry out of
+ * range counts in `bad` once for every child of its row. No output
  * may be an input, d_parent included. dq_pages_copy makes the copies, before
  * the next append. */
 int dq_pages_fork(const dq_tables *t, int64_t num_pages, const int32_t *d_refs,
