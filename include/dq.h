@@ -390,7 +390,8 @@ int dq_prefill_attention_paged(const dq_tables *t, const void *q, int q_dtype,
  * of itself, in two fp16 values to 2^-22 everywhere else, and never finer than
  * 2^-25.) A container whose fp16 norm is infinite
  * or NaN (a corrupt one) counts in integrity_errors and its norm as 0, so it
- * cannot reach the queries that do not see it. Everything else is as in
+ * cannot reach the queries that do not see it. A query row that holds a NaN or
+ * an infinity gives out = 0, as in the calls above. Everything else is as in
  * dq_decode_attention[_paged] (p = length - 1; the workspace is
  * dq_decode_workspace_bytes, length 0 gives out = 0) and in
  * dq_prefill_attention[_paged] (p = d_q_start[b] + i). The prefill workspace
