@@ -30,6 +30,7 @@ thread_local int g_last_cuda = 0;
 
 int cuda_fail(cudaError_t e) {
   g_last_cuda = static_cast<int>(e);
+  cudaGetLastError();  // (a call's error is not held against the next one, whose launches ask for the last error)
   return DQ_ERR_CUDA;
 }
 

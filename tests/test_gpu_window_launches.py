@@ -1,6 +1,8 @@
 """Launch forms of the windowed calls: calls one behind the other, captured
 ones, and ones beside each other on two streams, for both of the decode
 step's forms and for chunks."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -188,3 +190,31 @@ def test_a_query_that_is_not_finite_gives_zero_and_stays_with_its_row(value):
     want[rows], bound[rows] = 0.0, 0.0
     W.assert_within(_np(_prefill(lib, bad, kc[:2].contiguous(), vc[:2].contiguous(), [230, 0], 100, 4)), want, bound, False,
                     "chunk")
+
+
+def test_a_call_that_failed_does_not_fail_the_next_one():
+    # A call into a stream whose capture has been broken is refused by the runtime; the next call on another stream,
+    # whose launches ask for the last error, succeeds.
+    rt = ctypes.CDLL("libcudart.so.12")
+    lib = cm.lib_tables(2)
+    r, t, L = dq.new_page_state(8, 2, 4)
+    counts, ws = dq.new_page_counts(), torch.empty(dq.dq_pages_workspace_bytes(lib, 8, 2, 4), dtype=torch.uint8, device="cuda")
+    cache = dq.new_cache(1, 2, 32, 36)
+    k, zero = torch.randn(1, 2, 4, 128, device="cuda"), _ints([0])
+    seq, q = _ints([4]), torch.randn(1, 2, 128, device="cuda")
+    out, dws = torch.empty_like(q), _workspace(lib, 1, 2, 2, 32)
+    side, graph = torch.cuda.Stream(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(ctypes.c_void_p(side.cuda_stream), 0) == 0
+    try:
+        assert rt.cudaDeviceSynchronize() != 0  # (not allowed while a stream is captured: the capture is broken)
+        with pytest.raises(dq.DqError):
+            dq.dq_pages_advance(lib, r, t, L, L, r, t, L, counts, ws, stream=side)
+        with pytest.raises(dq.DqError):
+            dq.dq_decode_attention_window(lib, q, cache, cache, seq, 32, 8, 0, out, dws, stream=side)
+    finally:
+        rt.cudaStreamEndCapture(ctypes.c_void_p(side.cuda_stream), ctypes.byref(graph))
+        rt.cudaGetLastError()
+    dq.dq_append_kv(lib, k, k, zero, cache, cache.clone(), workspace=False)
+    dq.dq_pages_advance(lib, r, t, L, _ints([1, 1]), r, t, L, counts, ws)
+    assert L.tolist() == [1, 1]
