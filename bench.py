@@ -64,7 +64,7 @@ LAUNCHES_PER_STEP = 4
 # (Since that capture the file has changed in comments and in the windowed
 # instances only.)
 DECODE_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_decode.cu",
-                  "sha256_16": "b7bea06fb7063b17", "ck": 36, "cv": 36,
+                  "sha256_16": "32a9dc8c29627cf3", "ck": 36, "cv": 36,
                   "bytes_per_token_head": (151.367680e6 + 3.288064e6) / (32 * 8 * 8192)}
 
 
@@ -894,7 +894,7 @@ def prefill_launches_per_step(drift_mode):
 # only for that workload and container size while the kernel source matches.
 # (Since that capture the file has changed in comments and in the windowed
 # instances only.)
-PREFILL_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_prefill.cu", "sha256_16": "ae75fc9a99f72919",
+PREFILL_TRAFFIC = {"source": "decode_attention_dq_b200/csrc/dq_prefill.cu", "sha256_16": "8e01d2e42742f3b2",
                    "workload": "qwen3_8b_b16_t8k", "chunk": 512, "ck": 36, "cv": 36,
                    "bytes": 616.05e6 + 134.59e6}
 

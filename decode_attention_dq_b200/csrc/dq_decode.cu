@@ -51,7 +51,7 @@
 // window's first token on. Nothing else changes: the hidden groups take no
 // place in the order, their bytes and page-table entries are never read. What
 // bounds it is the passes through shared memory (91 % busy; 128 sequences x 8
-// KV heads, window 2048 + 64 first tokens, G = 4: 542 us, 2.2 M token-heads),
+// KV heads, window 2048 + 64 first tokens, G = 4: 544 us, 2.2 M token-heads),
 // as without a window; calls with few groups go to decode_few_kernel below.
 #include <cooperative_groups.h>
 
@@ -1245,7 +1245,7 @@ int few_capacity(int C, int n, size_t smem) {
 
 // Launches decode_few_kernel where it serves: the largest cluster with a pair
 // of warps for every group of a (b, h) and room for all (b, h) at once.
-// Returns -1 where there is none. (Against the balanced split: 14.4 and 25.7
+// Returns -1 where there is none. (Against the balanced split: 14.6 and 25.7
 // us for 8 rows of 34 groups, 17.6 and 28.0 us for 32; in two rounds of
 // clusters it is the slower one, 28.6 and 25.0 us for 16 rows of 65.)
 template <int G, bool kTwo, bool kLo>

@@ -72,8 +72,9 @@
 // 1.7e-3, P.V is half as many MMAs and the
 // softmax warps, which set the pace, have less to do per weight (3.1 thousand
 // cycles a block, 3.3 with hi + lo, at a higher clock; 16 sequences x 512 tokens x 8
-// KV heads, G = 4, window 1024: 445 us, 482 with hi + lo; 4 x 2048 tokens, G =
-// 8, window 4096: 926 us, 1070; 0.19 and 0.37 of the measured bf16 peak).
+// KV heads, G = 4, window 1024: 446 us, 482 with hi + lo; 4 x 2048 tokens, G =
+// 8, window 4096: 969 us, 1123 for fp32 outputs, which keep hi + lo; 0.19 and
+// 0.36 of the measured bf16 peak).
 // Every wait is bounded; a CTA that gives up counts it in wait_timeouts,
 // skips the rest of its work and still frees its tensor memory after its MMAs
 // and copies have drained.

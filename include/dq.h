@@ -440,6 +440,7 @@ int dq_prefill_attention_window_paged(const dq_tables *t, const void *q, int q_d
  * the host and a call can be captured in a graph. The results are whole
  * numbers determined by the state alone. One table and one refs array serve
  * all layers: page p of every layer's pool belongs to the same tokens.
+ *   t           for its device (and, in dq_pages_copy, its container sizes)
  *   num_pages   1 .. 2^31 - 1
  *   max_pages   pages per row, 1 .. 2^26 (a row's tokens are counted in int32)
  *   d_counts    device dq_page_counts, written by every call
